@@ -1,0 +1,664 @@
+// Objectives over rows of logits (include/kfac_objectives.h): label
+// log-probabilities, the clipped policy loss and the preference loss, the two
+// losses with the gradient of every logit.
+//
+// With s the logit scale, M = max_j x_j and S = sum_j exp(s (x_j - M)), a row
+// with label l has logp = s (x_l - M) - log S, and the gradient of
+// coef * logp is coef s (onehot(l) - exp(s (x - M)) / S).  All three are
+// bound by HBM: the logits in, the gradients out.
+//
+// Arithmetic: differences x - M are formed before scaling, so rows whose
+// logits are all huge, or all the type's lowest value, stay exact; exp is the
+// hardware's 2^x on a float32 argument; a vector's terms are added as a tree
+// in float32 and the vectors of a thread, the threads and the wavefronts in
+// 64 bits, in a fixed order; the gradient is rounded once, when it is stored.
+#include "objectives.h"
+
+#include <algorithm>
+
+namespace kfac {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kCus = 256;
+
+struct TokArgs {
+  const char* x;
+  char* g;
+  const void* labels;
+  float* logp;
+  int64_t rows;
+  int64_t ldx, ldg;    // bytes
+  int32_t vocab;
+  int32_t label_type;
+  float scale;         // s
+  float c;             // s log2(e): exp(s d) = 2^(c d)
+  float grad_scale;    // s grad_scale
+  uint32_t* flags;
+};
+
+struct PolArgs {
+  const float *adv, *weight, *old_logp, *ref;
+  double* part;        // [gridDim.x][3]
+  float lo, hi, kl;
+  float w0;            // weight where none is given
+};
+
+// Running maximum and sum of exp(s (x - max)) of some of a row's logits.
+struct Softmax {
+  float m;
+  double s;
+};
+
+// Adds the vectors v[0 .. N) to a thread's running maximum and sum.  Absent
+// values are minus infinity; `mu` replaces a maximum of minus infinity so
+// that those add exp(-inf) = 0.
+template <typename T, int N>
+__device__ inline void absorb(Softmax& a, const u32x4* v, float c) {
+  constexpr int VE = Elem<T>::VE;
+  float m = a.m;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < VE; i += 2) m = max3(m, Elem<T>::get(v[j], i), Elem<T>::get(v[j], i + 1));
+  const float mu = m == -INFINITY ? 0.f : m;
+  a.s *= static_cast<double>(__builtin_amdgcn_exp2f((a.m - mu) * c));
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    float e[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) e[i] = __builtin_amdgcn_exp2f((Elem<T>::get(v[j], i) - mu) * c);
+#pragma unroll
+    for (int w = VE / 2; w > 0; w >>= 1)
+#pragma unroll
+      for (int i = 0; i < w; ++i) e[i] += e[i + w];
+    a.s += static_cast<double>(e[0]);
+  }
+  a.m = m;
+}
+__device__ inline void absorb_one(Softmax& a, float x, float c) {
+  const float m = fmaxf(a.m, x);
+  const float mu = m == -INFINITY ? 0.f : m;
+  a.s = a.s * static_cast<double>(__builtin_amdgcn_exp2f((a.m - mu) * c)) +
+        static_cast<double>(__builtin_amdgcn_exp2f((x - mu) * c));
+  a.m = m;
+}
+
+// A team's maximum and sum from its threads'.  Several wavefronts meet in
+// `red`, whose two halves alternate from use to use (`parity`), so that one
+// barrier a row is enough.
+template <int TEAM>
+__device__ inline Softmax team_softmax(Softmax a, float c, Softmax* red, int parity) {
+  const float m = wave_max(a.m);
+  const float mu = m == -INFINITY ? 0.f : m;
+  Softmax r{m, wave_sum(a.s * static_cast<double>(__builtin_amdgcn_exp2f((a.m - mu) * c)))};
+  if constexpr (TEAM > kWave) {
+    constexpr int NW = TEAM / kWave;
+    const int lane = threadIdx.x & (kWave - 1);
+    red += parity * NW;
+    if (lane == 0) red[threadIdx.x / kWave] = r;
+    __syncthreads();
+    Softmax b{-INFINITY, 0.0};
+    if (lane < NW) b = red[lane];
+    r.m = lane_of(row_max(b.m), 0);
+    const float ru = r.m == -INFINITY ? 0.f : r.m;
+    r.s = lane_of(row_sum(b.s * static_cast<double>(__builtin_amdgcn_exp2f((b.m - ru) * c))), 0);
+  }
+  return r;
+}
+
+__device__ inline float log_prob(float xl, Softmax r, float scale) {
+  return (xl - r.m) * scale - logf(static_cast<float>(r.s));
+}
+
+// The label of a row, -1 for one to leave out (a label beyond the vocabulary
+// is reported and left out).
+__device__ inline int32_t row_label(const TokArgs& a, int64_t row) {
+  const int64_t l = load_index(a.labels, row, a.label_type);
+  if (l >= a.vocab) {
+    if ((threadIdx.x & (kWave - 1)) == 0) raise_flag(a.flags, KFAC_FLAG_BAD_INDEX);
+    return -1;
+  }
+  return l < 0 ? -1 : static_cast<int32_t>(l);
+}
+
+// coef / S times exp(s (x - M)), negated and rounded: a vector of the gradient.
+template <typename T>
+__device__ inline u32x4 grad_vec(u32x4 v, float m, float c, float neg) {
+  float o[Elem<T>::VE];
+#pragma unroll
+  for (int i = 0; i < Elem<T>::VE; ++i) o[i] = __builtin_amdgcn_exp2f((Elem<T>::get(v, i) - m) * c) * neg;
+  return pack16<T>(o);
+}
+template <typename T>
+__device__ inline float grad_one(float x, float m, float c, float neg) {
+  return __builtin_amdgcn_exp2f((x - m) * c) * neg;
+}
+
+// ---------------------------------------------------------------------------
+// Clipped policy loss: one team of wavefronts a row, the row held in
+// registers between its sum and its gradient, so each logit is read once and
+// each gradient written once.  A team walks rows a grid apart and asks for
+// the next row's vector in the place of each one it has finished, so loads
+// and stores stay mixed and no phase waits for an empty pipe.  LONG: rows
+// beyond the registers (TEAM * NV vectors) read the rest twice.
+
+struct RowScalars {
+  int32_t label;
+  float xl, w, adv, old_logp, ref;
+};
+
+template <typename T>
+__device__ inline RowScalars row_scalars(const TokArgs& a, const PolArgs& p, int64_t row, int32_t label) {
+  RowScalars r;
+  r.label = label;
+  r.xl = label >= 0 ? Elem<T>::load(a.x + row * a.ldx, label) : 0.f;
+  r.w = p.weight ? p.weight[row] : p.w0;
+  r.adv = p.adv[row];
+  r.old_logp = p.old_logp ? p.old_logp[row] : 0.f;
+  r.ref = p.ref ? p.ref[row] : 0.f;
+  return r;
+}
+
+template <typename T, int TEAM, int NV, bool LONG>
+__global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs a, PolArgs p) {
+  constexpr int VE = Elem<T>::VE;
+  constexpr int THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM, NW = TEAM / kWave;
+  constexpr int CH = NV < 4 ? NV : 4;
+  __shared__ Softmax red[2 * NW];
+  __shared__ double sums[TEAMS][3];
+  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM), tid = threadIdx.x % TEAM;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
+  const int nfull = a.vocab / VE, ntail = a.vocab % VE;
+  const float c = a.c;
+
+  u32x4 v[NV];
+  float tail = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) v[j] = u32x4{Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf};
+  double acc_a = 0.0, acc_k = 0.0, acc_c = 0.0;
+  bool bad = false;
+
+  int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
+  RowScalars cur{};
+  if (row < a.rows) {
+    const char* x = a.x + row * a.ldx;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (j * TEAM + tid < nfull) v[j] = load16(x + static_cast<int64_t>(j * TEAM + tid) * 16);
+    if (tid < ntail) tail = Elem<T>::load(x, static_cast<int64_t>(nfull) * VE + tid);
+    cur = row_scalars<T>(a, p, row, row_label(a, row));
+  }
+  int parity = 0;
+  while (row < a.rows) {
+    const int64_t next = row + stride;
+    const bool has = next < a.rows;
+    const int32_t nlabel = has ? row_label(a, next) : -1;
+    const char* xr = a.x + row * a.ldx;
+    const char* xn = a.x + next * a.ldx;
+    char* gr = a.g + row * a.ldg;
+
+    float coef = 0.f, neg = 0.f, logp = 0.f;
+    Softmax r{0.f, 1.0};
+    if (cur.label >= 0) {
+      Softmax t{-INFINITY, 0.0};
+#pragma unroll
+      for (int j = 0; j < NV; j += CH) absorb<T, CH>(t, v + j, c);
+      if (ntail) absorb_one(t, tail, c);
+      if constexpr (LONG) {
+        for (int j0 = NV; j0 * TEAM < nfull; j0 += CH) {
+          u32x4 u[CH];
+#pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            const int idx = (j0 + j) * TEAM + tid;
+            u[j] = u32x4{Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf};
+            if (idx < nfull) u[j] = load16(xr + static_cast<int64_t>(idx) * 16);
+          }
+          absorb<T, CH>(t, u, c);
+        }
+      }
+      r = team_softmax<TEAM>(t, c, red, parity);
+      parity ^= 1;
+      logp = log_prob(cur.xl, r, a.scale);
+      if (cur.w != 0.f) {
+        const float ratio = p.old_logp ? expf(logp - cur.old_logp) : 1.f;
+        const float held = fminf(fmaxf(ratio, p.lo), p.hi);
+        const float first = ratio * cur.adv, second = held * cur.adv;
+        const bool clipped = second < first;
+        const float gain = clipped ? second : first;
+        float slope = clipped ? 0.f : -first, kl = 0.f;
+        if (p.ref) {
+          const float d = cur.ref - logp, ed = expm1f(d);
+          kl = ed - d;
+          if (p.kl != 0.f) slope -= p.kl * ed;
+        }
+        const float w = cur.w;
+        coef = w * slope * a.grad_scale;
+        neg = -coef / static_cast<float>(r.s);
+        acc_a -= static_cast<double>(w) * gain;
+        acc_k += static_cast<double>(w) * kl;
+        acc_c += clipped ? w : 0.f;
+        bad |= !(fabsf(gain) < INFINITY && fabsf(kl) < INFINITY && fabsf(neg) < INFINITY);
+      }
+    }
+    if (tid == 0) a.logp[row] = logp;
+
+    const RowScalars nxt = has ? row_scalars<T>(a, p, next, nlabel) : RowScalars{};
+    const bool fetch = nlabel >= 0, zero = coef == 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int idx = j * TEAM + tid;
+      if (idx < nfull) {
+        const int64_t at = static_cast<int64_t>(idx) * 16;
+        store16(gr + at, zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(v[j], r.m, c, neg));
+        if (fetch) v[j] = load16(xn + at);
+      }
+    }
+    if constexpr (LONG) {
+      for (int idx = NV * TEAM + tid; idx < nfull; idx += TEAM) {
+        const int64_t at = static_cast<int64_t>(idx) * 16;
+        u32x4 o = {0u, 0u, 0u, 0u};
+        if (!zero) o = grad_vec<T>(load16(xr + at), r.m, c, neg);
+        store16(gr + at, o);
+      }
+    }
+    if (tid < ntail) {
+      const int64_t e = static_cast<int64_t>(nfull) * VE + tid;
+      Elem<T>::store(gr, e, zero ? 0.f : grad_one<T>(tail, r.m, c, neg));
+      if (fetch) tail = Elem<T>::load(xn, e);
+    }
+    // the label's entry, over what its owner has just stored there:
+    // coef (1 - p) with 1 - p = -expm1(logp), which does not cancel
+    if (!zero) {
+      const int lv = cur.label / VE;
+      const int owner = lv < nfull ? lv % TEAM : cur.label - nfull * VE;
+      if (tid == owner) Elem<T>::store(gr, cur.label, -coef * expm1f(logp));
+    }
+    row = next;
+    cur = nxt;
+  }
+  if (tid == 0) {
+    sums[team][0] = acc_a;
+    sums[team][1] = acc_k;
+    sums[team][2] = acc_c;
+    if (bad) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    double t = 0.0;
+    for (int i = 0; i < TEAMS; ++i) t += sums[i][threadIdx.x];
+    p.part[static_cast<int64_t>(blockIdx.x) * 3 + threadIdx.x] = t;
+  }
+}
+
+// stats from the workgroups' sums, added in a fixed order.
+__global__ void __launch_bounds__(256) policy_stats_kernel(const double* part, int n, float kl, float* stats) {
+  __shared__ double red[4][3];
+  double t[3] = {0.0, 0.0, 0.0};
+  for (int i = threadIdx.x; i < n; i += 256)
+    for (int q = 0; q < 3; ++q) t[q] += part[i * 3 + q];
+  for (int q = 0; q < 3; ++q) {
+    const double s = wave_sum(t[q]);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x / 64][q] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s[3];
+    for (int q = 0; q < 3; ++q) s[q] = (red[0][q] + red[1][q]) + (red[2][q] + red[3][q]);
+    stats[0] = static_cast<float>(kl != 0.f ? s[0] + static_cast<double>(kl) * s[1] : s[0]);
+    stats[1] = static_cast<float>(s[0]);
+    stats[2] = static_cast<float>(s[1]);
+    stats[3] = static_cast<float>(s[2]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Label log-probabilities: a team streams its row, UN vectors a thread at a
+// time.  With `stat` each row's (M, 1 / S) is kept for preference_grad_kernel.
+
+template <typename T, int TEAM, int UN>
+__global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) logp_kernel(TokArgs a, float2* stat, float* coef) {
+  constexpr int VE = Elem<T>::VE;
+  constexpr int THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM, NW = TEAM / kWave;
+  __shared__ Softmax red[2 * NW];
+  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM), tid = threadIdx.x % TEAM;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
+  const int nfull = a.vocab / VE, ntail = a.vocab % VE;
+  const float c = a.c;
+  int parity = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + team; row < a.rows; row += stride) {
+    const int32_t label = row_label(a, row);
+    float logp = 0.f;
+    Softmax r{0.f, 1.0};
+    if (label >= 0) {
+      const char* x = a.x + row * a.ldx;
+      const float xl = Elem<T>::load(x, label);
+      Softmax t{-INFINITY, 0.0};
+      for (int j0 = 0; j0 * TEAM < nfull; j0 += UN) {
+        u32x4 u[UN];
+#pragma unroll
+        for (int j = 0; j < UN; ++j) {
+          const int idx = (j0 + j) * TEAM + tid;
+          u[j] = u32x4{Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf};
+          if (idx < nfull) u[j] = load16(x + static_cast<int64_t>(idx) * 16);
+        }
+        absorb<T, UN>(t, u, c);
+      }
+      if (ntail) absorb_one(t, tid < ntail ? Elem<T>::load(x, static_cast<int64_t>(nfull) * VE + tid) : -INFINITY, c);
+      r = team_softmax<TEAM>(t, c, red, parity);
+      parity ^= 1;
+      logp = log_prob(xl, r, a.scale);
+    }
+    if (tid == 0) {
+      a.logp[row] = logp;
+      if (stat) {
+        stat[row] = make_float2(r.m, static_cast<float>(1.0 / r.s));
+        coef[row] = 0.f;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Preference loss, between its two passes over the logits: workgroup i adds
+// up pair i's log ratios and writes d loss / d logp of its rows.
+
+struct PrefArgs {
+  const int32_t* offsets;
+  const float *ref, *weight;
+  float* seq;
+  float* stats;
+  double* part;        // [pairs][4]
+  float* coef;         // [rows]
+  int32_t pairs, kind, average;
+  float beta, eps, w0;
+};
+
+constexpr int kPairThreads = 256;
+
+__device__ inline double block_sum(double v, double* red) {
+  v = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x / 64] = v;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+__device__ inline double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
+
+__global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a, PrefArgs p) {
+  __shared__ double red[4];
+  const int i = blockIdx.x;
+  double R[2], share[2];
+  int lo[2], hi[2];
+  for (int k = 0; k < 2; ++k) {
+    lo[k] = p.offsets[k * p.pairs + i];
+    hi[k] = p.offsets[k * p.pairs + i + 1];
+    if (lo[k] < 0 || hi[k] < lo[k] || hi[k] > a.rows) {
+      if (threadIdx.x == 0) raise_flag(a.flags, KFAC_FLAG_BAD_INDEX);
+      lo[k] = hi[k] = 0;
+    }
+    double s = 0.0, n = 0.0;
+    for (int r = lo[k] + threadIdx.x; r < hi[k]; r += kPairThreads) {
+      const int64_t l = load_index(a.labels, r, a.label_type);
+      if (l < 0 || l >= a.vocab) continue;
+      s += static_cast<double>(a.logp[r]) - (p.ref ? static_cast<double>(p.ref[r]) : 0.0);
+      n += 1.0;
+    }
+    s = block_sum(s, red);
+    n = block_sum(n, red);
+    share[k] = p.average ? (n > 0.0 ? 1.0 / n : 0.0) : 1.0;
+    R[k] = s * share[k];
+  }
+  const double h = R[0] - R[1], beta = p.beta, eps = p.eps;
+  const double w = p.weight ? static_cast<double>(p.weight[i]) : static_cast<double>(p.w0);
+  double loss, slope;
+  if (p.kind == KFAC_PREF_SIGMOID) {
+    const double x = beta * h;
+    loss = (1.0 - eps) * softplus(-x) + eps * softplus(x);
+    // sigma(x) - (1 - e), with sigma of the side that does not cancel
+    const double sig = 1.0 / (1.0 + exp(fabs(x)));    // sigma(-|x|)
+    slope = beta * (x >= 0.0 ? eps - sig : sig - (1.0 - eps));
+  } else {
+    const double x = h - 0.5 / beta;
+    loss = x * x;
+    slope = 2.0 * x;
+  }
+  if (threadIdx.x == 0) {
+    p.seq[i] = static_cast<float>(R[0]);
+    p.seq[p.pairs + i] = static_cast<float>(R[1]);
+    double* q = p.part + static_cast<int64_t>(i) * 4;
+    q[0] = w != 0.0 ? w * loss : 0.0;
+    q[1] = h > 0.0 ? w : 0.0;
+    q[2] = w != 0.0 ? w * beta * h : 0.0;
+    q[3] = w;
+    if (w != 0.0 && !(fabs(loss) < INFINITY)) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
+  }
+  for (int k = 0; k < 2; ++k) {
+    const double f = w != 0.0 ? (k ? -w : w) * slope * share[k] * static_cast<double>(a.grad_scale) : 0.0;
+    for (int r = lo[k] + threadIdx.x; r < hi[k]; r += kPairThreads) {
+      const int64_t l = load_index(a.labels, r, a.label_type);
+      p.coef[r] = l >= 0 && l < a.vocab ? static_cast<float>(f) : 0.f;
+    }
+  }
+}
+
+// Second pass over the logits: the gradient, from each row's (M, 1 / S) and
+// coefficient.  The rows are taken last to first, since the first pass leaves
+// its last rows in the 256 MB cache in front of the memory.  The extra
+// workgroup adds up the pairs' statistics.
+template <typename T, int TEAM, int UN>
+__global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) preference_grad_kernel(TokArgs a, PrefArgs p,
+                                                                                  const float2* stat) {
+  constexpr int VE = Elem<T>::VE;
+  constexpr int THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM;
+  if (blockIdx.x == 0) {
+    if (threadIdx.x < kWave) {
+      for (int q = 0; q < 4; ++q) {
+        double t = 0.0;
+        for (int i = threadIdx.x; i < p.pairs; i += kWave) t += p.part[static_cast<int64_t>(i) * 4 + q];
+        t = wave_sum(t);
+        if (threadIdx.x == 0) p.stats[q] = static_cast<float>(t);
+      }
+    }
+    return;
+  }
+  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM), tid = threadIdx.x % TEAM;
+  const int64_t stride = static_cast<int64_t>(gridDim.x - 1) * TEAMS;
+  const int nfull = a.vocab / VE, ntail = a.vocab % VE;
+  const float c = a.c;
+  for (int64_t back = static_cast<int64_t>(blockIdx.x - 1) * TEAMS + team; back < a.rows; back += stride) {
+    const int64_t row = a.rows - 1 - back;
+    const char* x = a.x + row * a.ldx;
+    char* g = a.g + row * a.ldg;
+    const float coef = p.coef[row];
+    const float2 ms = stat[row];
+    const bool zero = coef == 0.f;
+    const float neg = -coef * ms.y;
+    const int32_t label = zero ? -1 : row_label(a, row);
+    for (int j0 = 0; j0 * TEAM < nfull; j0 += UN) {
+      u32x4 u[UN];
+      if (!zero) {
+#pragma unroll
+        for (int j = 0; j < UN; ++j) {
+          const int idx = (j0 + j) * TEAM + tid;
+          if (idx < nfull) u[j] = load16(x + static_cast<int64_t>(idx) * 16);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < UN; ++j) {
+        const int idx = (j0 + j) * TEAM + tid;
+        if (idx < nfull)
+          store16(g + static_cast<int64_t>(idx) * 16, zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(u[j], ms.x, c, neg));
+      }
+    }
+    if (tid < ntail) {
+      const int64_t e = static_cast<int64_t>(nfull) * VE + tid;
+      Elem<T>::store(g, e, zero ? 0.f : grad_one<T>(Elem<T>::load(x, e), ms.x, c, neg));
+    }
+    if (!zero) {
+      const int lv = label / VE;
+      const int owner = lv < nfull ? lv % TEAM : label - nfull * VE;
+      if (tid == owner) Elem<T>::store(g, label, -coef * expm1f(a.logp[row]));
+    }
+  }
+}
+
+__global__ void zero_stats_kernel(float* stats) {
+  if (threadIdx.x < 4) stats[threadIdx.x] = 0.f;
+}
+
+TokArgs tok_args(const kfac_token_rows_t& t, char* ws) {
+  const int64_t el = t.dtype == KFAC_BF16 ? 2 : 4;
+  TokArgs a{};
+  a.x = static_cast<const char*>(t.logits);
+  a.g = static_cast<char*>(t.grad);
+  a.labels = t.labels;
+  a.logp = t.logp;
+  a.rows = t.rows;
+  a.ldx = t.ld * el;
+  a.ldg = t.grad_ld * el;
+  a.vocab = t.vocab;
+  a.label_type = t.label_type;
+  a.scale = t.logit_scale;
+  a.c = t.logit_scale * kLog2e;
+  a.grad_scale = t.logit_scale * t.grad_scale;
+  a.flags = reinterpret_cast<uint32_t*>(ws);
+  return a;
+}
+
+int grid_of(int64_t rows, int teams, int per_cu) {
+  return static_cast<int>(std::min<int64_t>((rows + teams - 1) / teams, static_cast<int64_t>(kCus) * per_cu));
+}
+
+template <typename T, int TEAM, int NV, bool LONG>
+int run_policy(const TokArgs& a, const PolArgs& p, int per_cu, hipStream_t st) {
+  constexpr int THREADS = TEAM < 256 ? 256 : TEAM;
+  const int grid = grid_of(a.rows, THREADS / TEAM, per_cu);
+  hipLaunchKernelGGL((policy_kernel<T, TEAM, NV, LONG>), dim3(grid), dim3(THREADS), 0, st, a, p);
+  return grid;
+}
+
+// The team and its registers by the row's length alone.
+template <typename T>
+int pick_policy(const TokArgs& a, const PolArgs& p, hipStream_t st) {
+  const int nvec = a.vocab / Elem<T>::VE;
+  if (nvec <= 64 * 4) return run_policy<T, 64, 4, false>(a, p, 6, st);
+  if (nvec <= 256 * 4) return run_policy<T, 256, 4, false>(a, p, 6, st);
+  if (nvec <= 256 * 8) return run_policy<T, 256, 8, false>(a, p, 5, st);
+  if (nvec <= 256 * 16) return run_policy<T, 256, 16, false>(a, p, 4, st);
+  if (nvec <= 1024 * 8) return run_policy<T, 1024, 8, false>(a, p, 1, st);
+  if (nvec <= 1024 * 16) return run_policy<T, 1024, 16, false>(a, p, 1, st);
+  return run_policy<T, 1024, 16, true>(a, p, 1, st);
+}
+
+template <typename T>
+void run_logp(const TokArgs& a, float2* stat, float* coef, hipStream_t st) {
+  const int nvec = a.vocab / Elem<T>::VE;
+  if (nvec <= 64 * 8)
+    hipLaunchKernelGGL((logp_kernel<T, 64, 4>), dim3(grid_of(a.rows, 4, 8)), dim3(256), 0, st, a, stat, coef);
+  else if (a.rows >= 2 * kCus)
+    hipLaunchKernelGGL((logp_kernel<T, 256, 8>), dim3(grid_of(a.rows, 1, 8)), dim3(256), 0, st, a, stat, coef);
+  else
+    hipLaunchKernelGGL((logp_kernel<T, 1024, 4>), dim3(grid_of(a.rows, 1, 2)), dim3(1024), 0, st, a, stat, coef);
+}
+
+template <typename T>
+void run_pref_grad(const TokArgs& a, const PrefArgs& p, const float2* stat, hipStream_t st) {
+  const int nvec = a.vocab / Elem<T>::VE;
+  if (nvec <= 64 * 8)
+    hipLaunchKernelGGL((preference_grad_kernel<T, 64, 4>), dim3(1 + grid_of(a.rows, 4, 8)), dim3(256), 0, st, a, p, stat);
+  else
+    hipLaunchKernelGGL((preference_grad_kernel<T, 256, 4>), dim3(1 + grid_of(a.rows, 1, 8)), dim3(256), 0, st, a, p, stat);
+}
+
+// Workspace behind the flag word.  policy: part [kMaxPartials][3] double.
+// preference: part [pairs][4] double, stat [rows] float2, coef [rows] float.
+struct PrefRegions {
+  size_t part, stat, coef, end;
+};
+PrefRegions pref_regions(int64_t rows, int32_t pairs) {
+  PrefRegions r;
+  r.part = kFlagBytes;
+  r.stat = r.part + align_up(static_cast<size_t>(pairs) * 4 * sizeof(double), 256);
+  r.coef = r.stat + align_up(static_cast<size_t>(rows) * sizeof(float2), 256);
+  r.end = r.coef + align_up(static_cast<size_t>(rows) * sizeof(float), 256);
+  return r;
+}
+
+}  // namespace
+
+size_t token_workspace_bytes(int objective, int64_t rows, int32_t groups) {
+  if (objective == KFAC_OBJ_POLICY) return kFlagBytes + align_up(sizeof(double) * 3 * kMaxPartials, 256);
+  if (objective == KFAC_OBJ_PREFERENCE) return pref_regions(rows, groups).end;
+  return kFlagBytes;
+}
+
+kfac_status_t launch_token_logp(const kfac_token_rows_t& t, char* ws, hipStream_t st) {
+  if (t.rows == 0) return KFAC_OK;
+  const TokArgs a = tok_args(t, ws);
+  if (t.dtype == KFAC_BF16) run_logp<__bf16>(a, nullptr, nullptr, st);
+  else run_logp<float>(a, nullptr, nullptr, st);
+  KFAC_HIP_TRY(hipGetLastError());
+  return KFAC_OK;
+}
+
+kfac_status_t launch_policy(const kfac_token_rows_t& t, const kfac_policy_t& p, char* ws, hipStream_t st) {
+  if (t.rows == 0) {
+    hipLaunchKernelGGL(zero_stats_kernel, dim3(1), dim3(64), 0, st, p.stats);
+    KFAC_HIP_TRY(hipGetLastError());
+    return KFAC_OK;
+  }
+  const TokArgs a = tok_args(t, ws);
+  PolArgs q{};
+  q.adv = p.advantage;
+  q.weight = p.weight;
+  q.old_logp = p.old_logp;
+  q.ref = p.ref_logp;
+  q.part = reinterpret_cast<double*>(ws + kFlagBytes);
+  q.lo = static_cast<float>(1.0 - static_cast<double>(p.clip_low));
+  q.hi = static_cast<float>(1.0 + static_cast<double>(p.clip_high));
+  q.kl = p.kl_coef;
+  q.w0 = static_cast<float>(1.0 / static_cast<double>(t.rows));
+  const int n = t.dtype == KFAC_BF16 ? pick_policy<__bf16>(a, q, st) : pick_policy<float>(a, q, st);
+  KFAC_HIP_TRY(hipGetLastError());
+  hipLaunchKernelGGL(policy_stats_kernel, dim3(1), dim3(256), 0, st, q.part, n, p.kl_coef, p.stats);
+  KFAC_HIP_TRY(hipGetLastError());
+  return KFAC_OK;
+}
+
+kfac_status_t launch_preference(const kfac_token_rows_t& t, const kfac_preference_t& p, char* ws, hipStream_t st) {
+  // with no rows every sequence is empty, and the losses at h = 0 still count
+  const TokArgs a = tok_args(t, ws);
+  const PrefRegions r = pref_regions(t.rows, p.pairs);
+  float2* stat = reinterpret_cast<float2*>(ws + r.stat);
+  PrefArgs q{};
+  q.offsets = p.offsets;
+  q.ref = p.ref_logp;
+  q.weight = p.pair_weight;
+  q.seq = p.seq;
+  q.stats = p.stats;
+  q.part = reinterpret_cast<double*>(ws + r.part);
+  q.coef = reinterpret_cast<float*>(ws + r.coef);
+  q.pairs = p.pairs;
+  q.kind = p.kind;
+  q.average = p.average;
+  q.beta = p.beta;
+  q.eps = p.kind == KFAC_PREF_SIGMOID ? p.label_smoothing : 0.f;
+  q.w0 = static_cast<float>(1.0 / p.pairs);
+  const bool half = t.dtype == KFAC_BF16;
+  if (t.rows > 0) {
+    if (half) run_logp<__bf16>(a, stat, q.coef, st);
+    else run_logp<float>(a, stat, q.coef, st);
+    KFAC_HIP_TRY(hipGetLastError());
+  }
+  hipLaunchKernelGGL(preference_pair_kernel, dim3(p.pairs), dim3(kPairThreads), 0, st, a, q);
+  KFAC_HIP_TRY(hipGetLastError());
+  if (half) run_pref_grad<__bf16>(a, q, stat, st);
+  else run_pref_grad<float>(a, q, stat, st);
+  KFAC_HIP_TRY(hipGetLastError());
+  return KFAC_OK;
+}
+
+}  // namespace kfac
