@@ -31,13 +31,13 @@ struct DropArgs {
 };
 
 // x of eight neighbours as floats, from whole vectors or (n < 8) one by one.
-template <typename T>
+template <typename T, bool NT>
 __device__ inline void load8(float (&f)[8], const char* p, int n) {
   if (n == 8) {
     constexpr int VE = Elem<T>::VE;
 #pragma unroll
     for (int q = 0; q < 8 / VE; ++q) {
-      const u32x4 v = load16(p + q * 16);
+      const u32x4 v = load16<NT>(p + q * 16);
 #pragma unroll
       for (int i = 0; i < VE; ++i) f[q * VE + i] = Elem<T>::get(v, i);
     }
@@ -47,7 +47,7 @@ __device__ inline void load8(float (&f)[8], const char* p, int n) {
   }
 }
 
-template <typename T, bool RES, int U>
+template <typename T, bool RES, bool NT, int U>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(DropArgs a) {
   constexpr int VE = Elem<T>::VE;
   const uint64_t off = a.offset + (a.offset_dev ? static_cast<uint64_t>(*a.offset_dev) : 0);
@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(DropArgs a) {
       }
       const int64_t at = static_cast<int64_t>(col) * (kBlockCols * sizeof(T));
       n[u] = col == a.per_row - 1 ? a.tail : kBlockCols;
-      load8<T>(x[u], a.x + row * a.ldx + at, n[u]);
-      if constexpr (RES) load8<T>(r[u], a.res + row * a.ldr + at, n[u]);
+      load8<T, NT>(x[u], a.x + row * a.ldx + at, n[u]);
+      if constexpr (RES) load8<T, NT>(r[u], a.res + row * a.ldr + at, n[u]);
       out[u] = a.y + row * a.ldy + at;
     }
   }
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(DropArgs a) {
     }
     if (n[u] == 8) {
 #pragma unroll
-      for (int q = 0; q < 8 / VE; ++q) store16(out[u] + q * 16, pack16<T>(o + q * VE));
+      for (int q = 0; q < 8 / VE; ++q) store16<NT>(out[u] + q * 16, pack16<T>(o + q * VE));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -117,8 +117,10 @@ template <typename T, bool RES>
 void run(const DropArgs& a, hipStream_t st) {
   constexpr int U = 2;
   const int64_t per = static_cast<int64_t>(kThreads) * U;
-  hipLaunchKernelGGL((dropout_kernel<T, RES, U>), dim3(static_cast<uint32_t>((a.blocks + per - 1) / per)),
-                     dim3(kThreads), 0, st, a);
+  const dim3 grid(static_cast<uint32_t>((a.blocks + per - 1) / per));
+  const bool nt = a.blocks * static_cast<int64_t>(kBlockCols * sizeof(T)) * (RES ? 3 : 2) > kCacheBytes;
+  if (nt) hipLaunchKernelGGL((dropout_kernel<T, RES, true, U>), grid, dim3(kThreads), 0, st, a);
+  else hipLaunchKernelGGL((dropout_kernel<T, RES, false, U>), grid, dim3(kThreads), 0, st, a);
 }
 
 }  // namespace

@@ -26,12 +26,26 @@ kfac_status_t launch_dropout(const kfac_dropout_t& d, hipStream_t st);
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // 16 bytes at any element alignment (gfx950 global accesses need none: one
-// 16-byte instruction, whatever the address).
-struct __attribute__((packed, aligned(2))) Bytes16 {
-  u32x4 v;
-};
-__device__ inline u32x4 load16(const void* p) { return static_cast<const Bytes16*>(p)->v; }
-__device__ inline void store16(void* p, u32x4 v) { static_cast<Bytes16*>(p)->v = v; }
+// 16-byte instruction, whatever the address).  NT: nontemporal, for data that
+// is not worth a place in the caches.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+template <bool NT = false>
+__device__ inline u32x4 load16(const void* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(static_cast<const u32x4_any*>(p));
+  else return *static_cast<const u32x4_any*>(p);
+}
+template <bool NT = false>
+__device__ inline void store16(void* p, u32x4 v) {
+  if constexpr (NT) __builtin_nontemporal_store(static_cast<u32x4_any>(v), static_cast<u32x4_any*>(p));
+  else *static_cast<u32x4_any*>(p) = v;
+}
+
+// The memory-side cache.  Streams that fit it together find what was written
+// just before and leave theirs for what comes next; larger ones go past it
+// with nontemporal accesses.  Measured on large copies and reads: 5.5 TB/s
+// and 6.3 TB/s through the cache, 6.0 and 7.1 past it (128 MB copied again
+// and again: 8.2 through it, 6.4 past it).
+constexpr int64_t kCacheBytes = int64_t(256) << 20;
 
 // Element type traits: VE elements per 16-byte vector.
 template <typename T>

@@ -15,12 +15,13 @@
 #include "objectives.h"
 
 #include <algorithm>
+#include <cfloat>
+#include <cmath>
 
 namespace kfac {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCus = 256;
 
 struct TokArgs {
@@ -34,6 +35,7 @@ struct TokArgs {
   int32_t label_type;
   float scale;         // s
   float c;             // s log2(e): exp(s d) = 2^(c d)
+  float clo;           // what c leaves of s log2(e)
   float grad_scale;    // s grad_scale
   uint32_t* flags;
 };
@@ -54,8 +56,16 @@ struct Softmax {
 // Adds the vectors v[0 .. N) to a thread's running maximum and sum.  Absent
 // values are minus infinity; `mu` replaces a maximum of minus infinity so
 // that those add exp(-inf) = 0.
-template <typename T, int N>
-__device__ inline void absorb(Softmax& a, const u32x4* v, float c) {
+// FINE multiplies by s log2(e) to twice float32's width: c alone is off by up
+// to 3e-8 of itself, which biases log S by that times the mean exponent, the
+// same way in every row; sums of log-probabilities over a sequence would show
+// it.  The gradients do without.
+template <bool FINE>
+__device__ inline float exp_of(float d, float c, float clo) {
+  return __builtin_amdgcn_exp2f(FINE ? fmaf(d, c, d * clo) : d * c);
+}
+template <typename T, int N, bool FINE = false>
+__device__ inline void absorb(Softmax& a, const u32x4* v, float c, float clo = 0.f) {
   constexpr int VE = Elem<T>::VE;
   float m = a.m;
 #pragma unroll
@@ -63,12 +73,12 @@ __device__ inline void absorb(Softmax& a, const u32x4* v, float c) {
 #pragma unroll
     for (int i = 0; i < VE; i += 2) m = max3(m, Elem<T>::get(v[j], i), Elem<T>::get(v[j], i + 1));
   const float mu = m == -INFINITY ? 0.f : m;
-  a.s *= static_cast<double>(__builtin_amdgcn_exp2f((a.m - mu) * c));
+  a.s *= static_cast<double>(exp_of<FINE>(a.m - mu, c, clo));
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     float e[VE];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) e[i] = __builtin_amdgcn_exp2f((Elem<T>::get(v[j], i) - mu) * c);
+    for (int i = 0; i < VE; ++i) e[i] = exp_of<FINE>(Elem<T>::get(v[j], i) - mu, c, clo);
 #pragma unroll
     for (int w = VE / 2; w > 0; w >>= 1)
 #pragma unroll
@@ -77,22 +87,22 @@ __device__ inline void absorb(Softmax& a, const u32x4* v, float c) {
   }
   a.m = m;
 }
-__device__ inline void absorb_one(Softmax& a, float x, float c) {
+template <bool FINE = false>
+__device__ inline void absorb_one(Softmax& a, float x, float c, float clo = 0.f) {
   const float m = fmaxf(a.m, x);
   const float mu = m == -INFINITY ? 0.f : m;
-  a.s = a.s * static_cast<double>(__builtin_amdgcn_exp2f((a.m - mu) * c)) +
-        static_cast<double>(__builtin_amdgcn_exp2f((x - mu) * c));
+  a.s = a.s * static_cast<double>(exp_of<FINE>(a.m - mu, c, clo)) + static_cast<double>(exp_of<FINE>(x - mu, c, clo));
   a.m = m;
 }
 
 // A team's maximum and sum from its threads'.  Several wavefronts meet in
 // `red`, whose two halves alternate from use to use (`parity`), so that one
 // barrier a row is enough.
-template <int TEAM>
-__device__ inline Softmax team_softmax(Softmax a, float c, Softmax* red, int parity) {
+template <int TEAM, bool FINE = false>
+__device__ inline Softmax team_softmax(Softmax a, float c, Softmax* red, int parity, float clo = 0.f) {
   const float m = wave_max(a.m);
   const float mu = m == -INFINITY ? 0.f : m;
-  Softmax r{m, wave_sum(a.s * static_cast<double>(__builtin_amdgcn_exp2f((a.m - mu) * c)))};
+  Softmax r{m, wave_sum(a.s * static_cast<double>(exp_of<FINE>(a.m - mu, c, clo)))};
   if constexpr (TEAM > kWave) {
     constexpr int NW = TEAM / kWave;
     const int lane = threadIdx.x & (kWave - 1);
@@ -103,7 +113,7 @@ __device__ inline Softmax team_softmax(Softmax a, float c, Softmax* red, int par
     if (lane < NW) b = red[lane];
     r.m = lane_of(row_max(b.m), 0);
     const float ru = r.m == -INFINITY ? 0.f : r.m;
-    r.s = lane_of(row_sum(b.s * static_cast<double>(__builtin_amdgcn_exp2f((b.m - ru) * c))), 0);
+    r.s = lane_of(row_sum(b.s * static_cast<double>(exp_of<FINE>(b.m - ru, c, clo))), 0);
   }
   return r;
 }
@@ -161,7 +171,7 @@ __device__ inline RowScalars row_scalars(const TokArgs& a, const PolArgs& p, int
   return r;
 }
 
-template <typename T, int TEAM, int NV, bool LONG>
+template <typename T, int TEAM, int NV, bool LONG, bool NT>
 __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs a, PolArgs p) {
   constexpr int VE = Elem<T>::VE;
   constexpr int THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM, NW = TEAM / kWave;
@@ -186,7 +196,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
     const char* x = a.x + row * a.ldx;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (j * TEAM + tid < nfull) v[j] = load16(x + static_cast<int64_t>(j * TEAM + tid) * 16);
+      if (j * TEAM + tid < nfull) v[j] = load16<NT>(x + static_cast<int64_t>(j * TEAM + tid) * 16);
     if (tid < ntail) tail = Elem<T>::load(x, static_cast<int64_t>(nfull) * VE + tid);
     cur = row_scalars<T>(a, p, row, row_label(a, row));
   }
@@ -213,7 +223,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
           for (int j = 0; j < CH; ++j) {
             const int idx = (j0 + j) * TEAM + tid;
             u[j] = u32x4{Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf};
-            if (idx < nfull) u[j] = load16(xr + static_cast<int64_t>(idx) * 16);
+            if (idx < nfull) u[j] = load16<NT>(xr + static_cast<int64_t>(idx) * 16);
           }
           absorb<T, CH>(t, u, c);
         }
@@ -251,16 +261,16 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
       const int idx = j * TEAM + tid;
       if (idx < nfull) {
         const int64_t at = static_cast<int64_t>(idx) * 16;
-        store16(gr + at, zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(v[j], r.m, c, neg));
-        if (fetch) v[j] = load16(xn + at);
+        store16<NT>(gr + at, zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(v[j], r.m, c, neg));
+        if (fetch) v[j] = load16<NT>(xn + at);
       }
     }
     if constexpr (LONG) {
       for (int idx = NV * TEAM + tid; idx < nfull; idx += TEAM) {
         const int64_t at = static_cast<int64_t>(idx) * 16;
         u32x4 o = {0u, 0u, 0u, 0u};
-        if (!zero) o = grad_vec<T>(load16(xr + at), r.m, c, neg);
-        store16(gr + at, o);
+        if (!zero) o = grad_vec<T>(load16<NT>(xr + at), r.m, c, neg);
+        store16<NT>(gr + at, o);
       }
     }
     if (tid < ntail) {
@@ -315,46 +325,63 @@ __global__ void __launch_bounds__(256) policy_stats_kernel(const double* part, i
 
 // ---------------------------------------------------------------------------
 // Label log-probabilities: a team streams its row, UN vectors a thread at a
-// time.  With `stat` each row's (M, 1 / S) is kept for preference_grad_kernel.
+// time.  logp is formed in 64 bits, since the preference loss adds up small
+// differences of it; with `stat` each row's (M, 1 / S) and with `wide` its logp
+// in 64 bits are kept for the kernels below.  Rows before `past` are read past
+// the cache.
+
+struct RowStats {
+  float2* stat;
+  double* wide;
+  float* coef;         // set to 0 for preference_pair_kernel
+  int64_t past;
+};
+
+template <typename T, int TEAM, int UN, bool NT>
+__device__ inline Softmax stream_row(const TokArgs& a, const char* x, int tid) {
+  constexpr int VE = Elem<T>::VE;
+  const int nfull = a.vocab / VE, ntail = a.vocab % VE;
+  Softmax t{-INFINITY, 0.0};
+  for (int j0 = 0; j0 * TEAM < nfull; j0 += UN) {
+    u32x4 u[UN];
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+      const int idx = (j0 + j) * TEAM + tid;
+      u[j] = u32x4{Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf};
+      if (idx < nfull) u[j] = load16<NT>(x + static_cast<int64_t>(idx) * 16);
+    }
+    absorb<T, UN, true>(t, u, a.c, a.clo);
+  }
+  if (ntail)
+    absorb_one<true>(t, tid < ntail ? Elem<T>::load(x, static_cast<int64_t>(nfull) * VE + tid) : -INFINITY, a.c, a.clo);
+  return t;
+}
 
 template <typename T, int TEAM, int UN>
-__global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) logp_kernel(TokArgs a, float2* stat, float* coef) {
-  constexpr int VE = Elem<T>::VE;
+__global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) logp_kernel(TokArgs a, RowStats out) {
   constexpr int THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM, NW = TEAM / kWave;
   __shared__ Softmax red[2 * NW];
   const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM), tid = threadIdx.x % TEAM;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
-  const int nfull = a.vocab / VE, ntail = a.vocab % VE;
-  const float c = a.c;
   int parity = 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + team; row < a.rows; row += stride) {
     const int32_t label = row_label(a, row);
-    float logp = 0.f;
+    double logp = 0.0;
     Softmax r{0.f, 1.0};
     if (label >= 0) {
       const char* x = a.x + row * a.ldx;
       const float xl = Elem<T>::load(x, label);
-      Softmax t{-INFINITY, 0.0};
-      for (int j0 = 0; j0 * TEAM < nfull; j0 += UN) {
-        u32x4 u[UN];
-#pragma unroll
-        for (int j = 0; j < UN; ++j) {
-          const int idx = (j0 + j) * TEAM + tid;
-          u[j] = u32x4{Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf};
-          if (idx < nfull) u[j] = load16(x + static_cast<int64_t>(idx) * 16);
-        }
-        absorb<T, UN>(t, u, c);
-      }
-      if (ntail) absorb_one(t, tid < ntail ? Elem<T>::load(x, static_cast<int64_t>(nfull) * VE + tid) : -INFINITY, c);
-      r = team_softmax<TEAM>(t, c, red, parity);
+      Softmax t = row < out.past ? stream_row<T, TEAM, UN, true>(a, x, tid) : stream_row<T, TEAM, UN, false>(a, x, tid);
+      r = team_softmax<TEAM, true>(t, a.c, red, parity, a.clo);
       parity ^= 1;
-      logp = log_prob(xl, r, a.scale);
+      if (tid == 0) logp = (static_cast<double>(xl) - static_cast<double>(r.m)) * static_cast<double>(a.scale) - log(r.s);
     }
     if (tid == 0) {
-      a.logp[row] = logp;
-      if (stat) {
-        stat[row] = make_float2(r.m, static_cast<float>(1.0 / r.s));
-        coef[row] = 0.f;
+      a.logp[row] = static_cast<float>(logp);
+      if (out.stat) {
+        out.stat[row] = make_float2(r.m, static_cast<float>(1.0 / r.s));
+        out.wide[row] = logp;
+        out.coef[row] = 0.f;
       }
     }
   }
@@ -370,7 +397,8 @@ struct PrefArgs {
   float* seq;
   float* stats;
   double* part;        // [pairs][4]
-  float* coef;         // [rows]
+  const double* wide;  // [rows]: logp
+  float* coef;         // [rows], zero before preference_pair_kernel
   int32_t pairs, kind, average;
   float beta, eps, w0;
 };
@@ -403,7 +431,7 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a
     for (int r = lo[k] + threadIdx.x; r < hi[k]; r += kPairThreads) {
       const int64_t l = load_index(a.labels, r, a.label_type);
       if (l < 0 || l >= a.vocab) continue;
-      s += static_cast<double>(a.logp[r]) - (p.ref ? static_cast<double>(p.ref[r]) : 0.0);
+      s += p.wide[r] - (p.ref ? static_cast<double>(p.ref[r]) : 0.0);
       n += 1.0;
     }
     s = block_sum(s, red);
@@ -445,12 +473,36 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a
 }
 
 // Second pass over the logits: the gradient, from each row's (M, 1 / S) and
-// coefficient.  The rows are taken last to first, since the first pass leaves
-// its last rows in the 256 MB cache in front of the memory.  The extra
+// coefficient.  The rows are taken last to first: where logits and gradients
+// do not fit the cache, the first pass reads all but its last rows past it
+// and the gradients are stored past it, so that those last rows are still
+// there (287 -> 213 us on 7200 rows of 32768 bf16 logits).  The extra
 // workgroup adds up the pairs' statistics.
-template <typename T, int TEAM, int UN>
+template <typename T, int TEAM, int UN, bool NTL, bool NTS>
+__device__ inline void grad_row(const TokArgs& a, const char* x, char* g, int tid, float m, float neg, bool zero) {
+  const int nfull = a.vocab / Elem<T>::VE;
+  for (int j0 = 0; j0 * TEAM < nfull; j0 += UN) {
+    u32x4 u[UN];
+    if (!zero) {
+#pragma unroll
+      for (int j = 0; j < UN; ++j) {
+        const int idx = (j0 + j) * TEAM + tid;
+        if (idx < nfull) u[j] = load16<NTL>(x + static_cast<int64_t>(idx) * 16);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+      const int idx = (j0 + j) * TEAM + tid;
+      if (idx < nfull)
+        store16<NTS>(g + static_cast<int64_t>(idx) * 16,
+                     zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(u[j], m, a.c, neg));
+    }
+  }
+}
+
+template <typename T, int TEAM, int UN, bool NT>
 __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) preference_grad_kernel(TokArgs a, PrefArgs p,
-                                                                                  const float2* stat) {
+                                                                                  RowStats rs) {
   constexpr int VE = Elem<T>::VE;
   constexpr int THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM;
   if (blockIdx.x == 0) {
@@ -467,35 +519,20 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) preference_grad_kerne
   const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM), tid = threadIdx.x % TEAM;
   const int64_t stride = static_cast<int64_t>(gridDim.x - 1) * TEAMS;
   const int nfull = a.vocab / VE, ntail = a.vocab % VE;
-  const float c = a.c;
   for (int64_t back = static_cast<int64_t>(blockIdx.x - 1) * TEAMS + team; back < a.rows; back += stride) {
     const int64_t row = a.rows - 1 - back;
     const char* x = a.x + row * a.ldx;
     char* g = a.g + row * a.ldg;
     const float coef = p.coef[row];
-    const float2 ms = stat[row];
+    const float2 ms = rs.stat[row];
     const bool zero = coef == 0.f;
     const float neg = -coef * ms.y;
     const int32_t label = zero ? -1 : row_label(a, row);
-    for (int j0 = 0; j0 * TEAM < nfull; j0 += UN) {
-      u32x4 u[UN];
-      if (!zero) {
-#pragma unroll
-        for (int j = 0; j < UN; ++j) {
-          const int idx = (j0 + j) * TEAM + tid;
-          if (idx < nfull) u[j] = load16(x + static_cast<int64_t>(idx) * 16);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < UN; ++j) {
-        const int idx = (j0 + j) * TEAM + tid;
-        if (idx < nfull)
-          store16(g + static_cast<int64_t>(idx) * 16, zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(u[j], ms.x, c, neg));
-      }
-    }
+    if (NT && row < rs.past) grad_row<T, TEAM, UN, true, NT>(a, x, g, tid, ms.x, neg, zero);
+    else grad_row<T, TEAM, UN, false, NT>(a, x, g, tid, ms.x, neg, zero);
     if (tid < ntail) {
       const int64_t e = static_cast<int64_t>(nfull) * VE + tid;
-      Elem<T>::store(g, e, zero ? 0.f : grad_one<T>(Elem<T>::load(x, e), ms.x, c, neg));
+      Elem<T>::store(g, e, zero ? 0.f : grad_one<T>(Elem<T>::load(x, e), ms.x, a.c, neg));
     }
     if (!zero) {
       const int lv = label / VE;
@@ -522,7 +559,12 @@ TokArgs tok_args(const kfac_token_rows_t& t, char* ws) {
   a.vocab = t.vocab;
   a.label_type = t.label_type;
   a.scale = t.logit_scale;
-  a.c = t.logit_scale * kLog2e;
+  const double c = static_cast<double>(t.logit_scale) * 1.4426950408889634;
+  a.c = static_cast<float>(c);
+  // c below the exact product and clo above 0, so that a difference of minus
+  // infinity stays one in d c + d clo
+  if (static_cast<double>(a.c) >= c) a.c = std::nextafter(a.c, 0.f);
+  a.clo = std::max(static_cast<float>(c - static_cast<double>(a.c)), FLT_MIN);
   a.grad_scale = t.logit_scale * t.grad_scale;
   a.flags = reinterpret_cast<uint32_t*>(ws);
   return a;
@@ -536,7 +578,11 @@ template <typename T, int TEAM, int NV, bool LONG>
 int run_policy(const TokArgs& a, const PolArgs& p, int per_cu, hipStream_t st) {
   constexpr int THREADS = TEAM < 256 ? 256 : TEAM;
   const int grid = grid_of(a.rows, THREADS / TEAM, per_cu);
-  hipLaunchKernelGGL((policy_kernel<T, TEAM, NV, LONG>), dim3(grid), dim3(THREADS), 0, st, a, p);
+  // the part of a LONG row that is read again is best left in the cache
+  if (!LONG && 2 * a.rows * a.vocab * static_cast<int64_t>(sizeof(T)) > kCacheBytes)
+    hipLaunchKernelGGL((policy_kernel<T, TEAM, NV, LONG, !LONG>), dim3(grid), dim3(THREADS), 0, st, a, p);
+  else
+    hipLaunchKernelGGL((policy_kernel<T, TEAM, NV, LONG, false>), dim3(grid), dim3(THREADS), 0, st, a, p);
   return grid;
 }
 
@@ -554,35 +600,56 @@ int pick_policy(const TokArgs& a, const PolArgs& p, hipStream_t st) {
 }
 
 template <typename T>
-void run_logp(const TokArgs& a, float2* stat, float* coef, hipStream_t st) {
+void run_logp(const TokArgs& a, const RowStats& rs, hipStream_t st) {
   const int nvec = a.vocab / Elem<T>::VE;
   if (nvec <= 64 * 8)
-    hipLaunchKernelGGL((logp_kernel<T, 64, 4>), dim3(grid_of(a.rows, 4, 8)), dim3(256), 0, st, a, stat, coef);
+    hipLaunchKernelGGL((logp_kernel<T, 64, 4>), dim3(grid_of(a.rows, 4, 8)), dim3(256), 0, st, a, rs);
   else if (a.rows >= 2 * kCus)
-    hipLaunchKernelGGL((logp_kernel<T, 256, 8>), dim3(grid_of(a.rows, 1, 8)), dim3(256), 0, st, a, stat, coef);
+    hipLaunchKernelGGL((logp_kernel<T, 256, 8>), dim3(grid_of(a.rows, 1, 8)), dim3(256), 0, st, a, rs);
   else
-    hipLaunchKernelGGL((logp_kernel<T, 1024, 4>), dim3(grid_of(a.rows, 1, 2)), dim3(1024), 0, st, a, stat, coef);
+    hipLaunchKernelGGL((logp_kernel<T, 1024, 4>), dim3(grid_of(a.rows, 1, 2)), dim3(1024), 0, st, a, rs);
+}
+
+template <typename T, bool NT>
+void run_pref_grad(const TokArgs& a, const PrefArgs& p, const RowStats& rs, hipStream_t st) {
+  const int nvec = a.vocab / Elem<T>::VE;
+  if (nvec <= 64 * 8)
+    hipLaunchKernelGGL((preference_grad_kernel<T, 64, 4, NT>), dim3(1 + grid_of(a.rows, 4, 8)), dim3(256), 0, st, a,
+                       p, rs);
+  else
+    hipLaunchKernelGGL((preference_grad_kernel<T, 256, 4, NT>), dim3(1 + grid_of(a.rows, 1, 8)), dim3(256), 0, st, a,
+                       p, rs);
 }
 
 template <typename T>
-void run_pref_grad(const TokArgs& a, const PrefArgs& p, const float2* stat, hipStream_t st) {
-  const int nvec = a.vocab / Elem<T>::VE;
-  if (nvec <= 64 * 8)
-    hipLaunchKernelGGL((preference_grad_kernel<T, 64, 4>), dim3(1 + grid_of(a.rows, 4, 8)), dim3(256), 0, st, a, p, stat);
-  else
-    hipLaunchKernelGGL((preference_grad_kernel<T, 256, 4>), dim3(1 + grid_of(a.rows, 1, 8)), dim3(256), 0, st, a, p, stat);
+kfac_status_t run_preference(const TokArgs& a, const PrefArgs& q, RowStats rs, hipStream_t st) {
+  const int64_t row_bytes = static_cast<int64_t>(a.vocab) * sizeof(T);
+  const bool nt = 2 * a.rows * row_bytes > kCacheBytes;
+  rs.past = nt ? std::max<int64_t>(0, a.rows - kCacheBytes * 3 / 4 / row_bytes) : 0;
+  if (a.rows > 0) {
+    run_logp<T>(a, rs, st);
+    KFAC_HIP_TRY(hipGetLastError());
+  }
+  hipLaunchKernelGGL(preference_pair_kernel, dim3(q.pairs), dim3(kPairThreads), 0, st, a, q);
+  KFAC_HIP_TRY(hipGetLastError());
+  if (nt) run_pref_grad<T, true>(a, q, rs, st);
+  else run_pref_grad<T, false>(a, q, rs, st);
+  KFAC_HIP_TRY(hipGetLastError());
+  return KFAC_OK;
 }
 
 // Workspace behind the flag word.  policy: part [kMaxPartials][3] double.
-// preference: part [pairs][4] double, stat [rows] float2, coef [rows] float.
+// preference: part [pairs][4] double, stat [rows] float2, wide [rows] double,
+// coef [rows] float.
 struct PrefRegions {
-  size_t part, stat, coef, end;
+  size_t part, stat, wide, coef, end;
 };
 PrefRegions pref_regions(int64_t rows, int32_t pairs) {
   PrefRegions r;
   r.part = kFlagBytes;
   r.stat = r.part + align_up(static_cast<size_t>(pairs) * 4 * sizeof(double), 256);
-  r.coef = r.stat + align_up(static_cast<size_t>(rows) * sizeof(float2), 256);
+  r.wide = r.stat + align_up(static_cast<size_t>(rows) * sizeof(float2), 256);
+  r.coef = r.wide + align_up(static_cast<size_t>(rows) * sizeof(double), 256);
   r.end = r.coef + align_up(static_cast<size_t>(rows) * sizeof(float), 256);
   return r;
 }
@@ -598,8 +665,10 @@ size_t token_workspace_bytes(int objective, int64_t rows, int32_t groups) {
 kfac_status_t launch_token_logp(const kfac_token_rows_t& t, char* ws, hipStream_t st) {
   if (t.rows == 0) return KFAC_OK;
   const TokArgs a = tok_args(t, ws);
-  if (t.dtype == KFAC_BF16) run_logp<__bf16>(a, nullptr, nullptr, st);
-  else run_logp<float>(a, nullptr, nullptr, st);
+  // each logit is read once: past the cache, which serves reads as fast at any size
+  const RowStats rs{nullptr, nullptr, nullptr, t.rows};
+  if (t.dtype == KFAC_BF16) run_logp<__bf16>(a, rs, st);
+  else run_logp<float>(a, rs, st);
   KFAC_HIP_TRY(hipGetLastError());
   return KFAC_OK;
 }
@@ -632,7 +701,6 @@ kfac_status_t launch_preference(const kfac_token_rows_t& t, const kfac_preferenc
   // with no rows every sequence is empty, and the losses at h = 0 still count
   const TokArgs a = tok_args(t, ws);
   const PrefRegions r = pref_regions(t.rows, p.pairs);
-  float2* stat = reinterpret_cast<float2*>(ws + r.stat);
   PrefArgs q{};
   q.offsets = p.offsets;
   q.ref = p.ref_logp;
@@ -647,18 +715,12 @@ kfac_status_t launch_preference(const kfac_token_rows_t& t, const kfac_preferenc
   q.beta = p.beta;
   q.eps = p.kind == KFAC_PREF_SIGMOID ? p.label_smoothing : 0.f;
   q.w0 = static_cast<float>(1.0 / p.pairs);
-  const bool half = t.dtype == KFAC_BF16;
-  if (t.rows > 0) {
-    if (half) run_logp<__bf16>(a, stat, q.coef, st);
-    else run_logp<float>(a, stat, q.coef, st);
-    KFAC_HIP_TRY(hipGetLastError());
-  }
-  hipLaunchKernelGGL(preference_pair_kernel, dim3(p.pairs), dim3(kPairThreads), 0, st, a, q);
-  KFAC_HIP_TRY(hipGetLastError());
-  if (half) run_pref_grad<__bf16>(a, q, stat, st);
-  else run_pref_grad<float>(a, q, stat, st);
-  KFAC_HIP_TRY(hipGetLastError());
-  return KFAC_OK;
+  RowStats rs{};
+  rs.stat = reinterpret_cast<float2*>(ws + r.stat);
+  rs.wide = reinterpret_cast<double*>(ws + r.wide);
+  rs.coef = q.coef;
+  q.wide = rs.wide;
+  return t.dtype == KFAC_BF16 ? run_preference<__bf16>(a, q, rs, st) : run_preference<float>(a, q, rs, st);
 }
 
 }  // namespace kfac

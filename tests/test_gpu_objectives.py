@@ -224,6 +224,30 @@ def test_masked_columns_and_rows(Q, vocab, dtype):
     assert op.flags() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [13, 1000, 9001, 70001])
+def test_masked_columns_in_sequences(Q, vocab, dtype):
+    """The same columns in the log-probabilities and the preference loss, at several scales."""
+    rng = np.random.default_rng(4)
+    x, _ = matrix(rng, 4, vocab, dtype)
+    x[0, 1:vocab // 2] = -float("inf")
+    x[1, 1:vocab // 2] = torch.finfo(DT[dtype]).min
+    x[2, :] = torch.finfo(DT[dtype]).min
+    labels = np.array([0, vocab - 1, 5, 3])
+    xd = wide(x)
+    xt = np.where(np.isfinite(xd) & (xd > -1e30), xd, 0.0)
+    for s in (1.0, 0.7, 2.0):
+        want = O.token_logp(xd, labels, s)
+        near(Q.TokenLogp(4, vocab, dtype, logit_scale=s).run(x, gpu(labels)), want, logp_tolerance(xt, labels, s) + 1e-6)
+        op = Q.PreferenceLoss(4, 1, vocab, dtype, logit_scale=s)
+        stats, seq, logp, grad = op.run(x, gpu(labels), gpu([0, 2, 4], torch.int32))
+        wstats, wseq, _, wgrad = O.preference_loss(xd, labels, [0, 2, 4], beta=float(np.float32(0.1)), s=s)
+        near(seq, wseq, 2 * (logp_tolerance(xt, labels, s).sum() + 1e-6))
+        near(stats, wstats, 1e-5)
+        near(grad, wgrad, HALF[dtype] * np.abs(wgrad) + 1e-5)
+        assert op.flags() == 0
+
+
 def test_nonfinite_and_bad_labels_are_flagged(Q):
     x = torch.zeros(4, 50, device="cuda")
     x[1, 3] = float("nan")
