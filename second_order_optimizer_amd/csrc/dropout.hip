@@ -1,8 +1,8 @@
 // Dropout from a counter-based generator (include/kfac_objectives.h): the
 // mask is computed where it is needed, forward and backward, and never
-// stored.  One thread makes one Philox 4x32-10 block, eight 16-bit draws, for
-// eight neighbours of a row: 16 bytes of bf16, 32 of float32.  Bound by HBM:
-// x (and the residual) in, y out.
+// stored.  One Philox 4x32-10 block is eight 16-bit draws for eight
+// neighbours of a row: 16 bytes of bf16, 32 of float32.  Bound by HBM: x (and
+// the residual) in, y out.
 #include "objectives.h"
 
 #include <algorithm>
@@ -14,6 +14,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlockCols = 8;     // draws of one generator block
+// Passes of more than this go past the cache: 8192 x 4096 bf16 forward with
+// residual and backward 69 -> 59 us (U = 4 chunks a thread: 76 -> 62).
+constexpr int64_t kStreamBytes = kCacheBytes / 4;
 
 struct DropArgs {
   const char* x;
@@ -30,34 +33,59 @@ struct DropArgs {
   float scale;
 };
 
-// x of eight neighbours as floats, from whole vectors or (n < 8) one by one.
+// Four words of the generator for one block.
+__device__ inline void philox(uint64_t block, uint64_t off, uint32_t k0, uint32_t k1, uint32_t (&c)[4]) {
+  c[0] = static_cast<uint32_t>(block);
+  c[1] = static_cast<uint32_t>(block >> 32);
+  c[2] = static_cast<uint32_t>(off);
+  c[3] = static_cast<uint32_t>(off >> 32);
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c[0], p1 = static_cast<uint64_t>(0xCD9E8D57u) * c[2];
+    c[0] = static_cast<uint32_t>(p1 >> 32) ^ c[1] ^ k0;
+    c[1] = static_cast<uint32_t>(p1);
+    c[2] = static_cast<uint32_t>(p0 >> 32) ^ c[3] ^ k1;
+    c[3] = static_cast<uint32_t>(p0);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+__device__ inline uint32_t swap_pair(uint32_t v) { return __builtin_amdgcn_update_dpp(0, v, kXor1, 0xF, 0xF, true); }
+
+// VE neighbours as floats: one vector, or (n < VE) one by one.
 template <typename T, bool NT>
-__device__ inline void load8(float (&f)[8], const char* p, int n) {
-  if (n == 8) {
-    constexpr int VE = Elem<T>::VE;
+__device__ inline void load_some(float (&f)[Elem<T>::VE], const char* p, int n) {
+  constexpr int VE = Elem<T>::VE;
+  if (n == VE) {
+    const u32x4 v = load16<NT>(p);
 #pragma unroll
-    for (int q = 0; q < 8 / VE; ++q) {
-      const u32x4 v = load16<NT>(p + q * 16);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) f[q * VE + i] = Elem<T>::get(v, i);
-    }
+    for (int i = 0; i < VE; ++i) f[i] = Elem<T>::get(v, i);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < n ? Elem<T>::load(p, i) : 0.f;
+    for (int i = 0; i < VE; ++i) f[i] = i < n ? Elem<T>::load(p, i) : 0.f;
   }
 }
 
+// A thread works on U chunks of 16 bytes.  bf16: a chunk is a generator block.
+// float32: a chunk is half of one, and to keep a wavefront's accesses in one
+// run the two halves of a block sit in neighbouring lanes; each lane of such a
+// pair makes one block for two chunks, 32 blocks apart, and they exchange the
+// halves.
 template <typename T, bool RES, bool NT, int U>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(DropArgs a) {
   constexpr int VE = Elem<T>::VE;
+  constexpr bool HALVES = VE < kBlockCols;
+  constexpr int GROUPS = HALVES ? U / 2 : U;      // generator blocks a thread makes
   const uint64_t off = a.offset + (a.offset_dev ? static_cast<uint64_t>(*a.offset_dev) : 0);
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * U) + threadIdx.x;
-  float x[U][8], r[U][8];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * GROUPS);
+  const int lane = threadIdx.x & (kWave - 1), odd = lane & 1;
+  const int64_t wave = first + (threadIdx.x & ~(kWave - 1));
+  float x[U][VE], r[U][VE];
   int n[U];
   char* out[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t b = first + u * kThreads;
+    const int64_t b = HALVES ? wave + (u / 2) * kThreads + (u & 1) * 32 + (lane >> 1) : first + u * kThreads + threadIdx.x;
     n[u] = 0;
     if (b < a.blocks) {
       int64_t row;
@@ -70,45 +98,50 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(DropArgs a) {
         row = b / a.per_row;
         col = static_cast<uint32_t>(b - row * a.per_row);
       }
-      const int64_t at = static_cast<int64_t>(col) * (kBlockCols * sizeof(T));
-      n[u] = col == a.per_row - 1 ? a.tail : kBlockCols;
-      load8<T, NT>(x[u], a.x + row * a.ldx + at, n[u]);
-      if constexpr (RES) load8<T, NT>(r[u], a.res + row * a.ldr + at, n[u]);
+      const int lead = HALVES ? odd * VE : 0;
+      const int64_t at = (static_cast<int64_t>(col) * kBlockCols + lead) * static_cast<int64_t>(sizeof(T));
+      n[u] = col == a.per_row - 1 ? max(0, min(VE, static_cast<int>(a.tail) - lead)) : VE;
+      load_some<T, NT>(x[u], a.x + row * a.ldx + at, n[u]);
+      if constexpr (RES) load_some<T, NT>(r[u], a.res + row * a.ldr + at, n[u]);
       out[u] = a.y + row * a.ldy + at;
     }
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (n[u] == 0) continue;
-    const uint64_t b = static_cast<uint64_t>(first + u * kThreads);
-    uint32_t c0 = static_cast<uint32_t>(b), c1 = static_cast<uint32_t>(b >> 32);
-    uint32_t c2 = static_cast<uint32_t>(off), c3 = static_cast<uint32_t>(off >> 32);
-    uint32_t k0 = a.k0, k1 = a.k1;
+  for (int k = 0; k < GROUPS; ++k) {
+    uint32_t c[4];
+    const int64_t b = HALVES ? wave + k * kThreads + odd * 32 + (lane >> 1) : first + k * kThreads + threadIdx.x;
+    philox(static_cast<uint64_t>(b), off, a.k0, a.k1, c);
+    uint32_t words[HALVES ? 2 : 1][VE / 2];       // the draws of this group's chunks
+    if constexpr (HALVES) {
 #pragma unroll
-    for (int i = 0; i < 10; ++i) {
-      const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0, p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
-      c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
-      c1 = static_cast<uint32_t>(p1);
-      c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
-      c3 = static_cast<uint32_t>(p0);
-      k0 += 0x9E3779B9u;
-      k1 += 0xBB67AE85u;
-    }
-    const uint32_t c[4] = {c0, c1, c2, c3};
-    float o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t draw = (i & 1) ? c[i >> 1] >> 16 : c[i >> 1] & 0xFFFFu;
-      o[i] = draw >= a.threshold ? x[u][i] * a.scale : 0.f;
-      if constexpr (RES) o[i] += r[u][i];
-    }
-    if (n[u] == 8) {
-#pragma unroll
-      for (int q = 0; q < 8 / VE; ++q) store16<NT>(out[u] + q * 16, pack16<T>(o + q * VE));
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t own = odd ? c[2 + i] : c[i];
+        const uint32_t got = swap_pair(odd ? c[i] : c[2 + i]);
+        words[0][i] = odd ? got : own;
+        words[1][i] = odd ? own : got;
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n[u]) Elem<T>::store(out[u], i, o[i]);
+      for (int i = 0; i < 4; ++i) words[0][i] = c[i];
+    }
+#pragma unroll
+    for (int h = 0; h < (HALVES ? 2 : 1); ++h) {
+      const int u = HALVES ? 2 * k + h : k;
+      if (n[u] == 0) continue;
+      float o[VE];
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const uint32_t draw = (i & 1) ? words[h][i >> 1] >> 16 : words[h][i >> 1] & 0xFFFFu;
+        o[i] = draw >= a.threshold ? x[u][i] * a.scale : 0.f;
+        if constexpr (RES) o[i] += r[u][i];
+      }
+      if (n[u] == VE) {
+        store16<NT>(out[u], pack16<T>(o));
+      } else {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if (i < n[u]) Elem<T>::store(out[u], i, o[i]);
+      }
     }
   }
 }
@@ -116,9 +149,9 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(DropArgs a) {
 template <typename T, bool RES>
 void run(const DropArgs& a, hipStream_t st) {
   constexpr int U = 2;
-  const int64_t per = static_cast<int64_t>(kThreads) * U;
+  const int64_t per = static_cast<int64_t>(kThreads) * U * Elem<T>::VE / kBlockCols;
   const dim3 grid(static_cast<uint32_t>((a.blocks + per - 1) / per));
-  const bool nt = a.blocks * static_cast<int64_t>(kBlockCols * sizeof(T)) * (RES ? 3 : 2) > kCacheBytes;
+  const bool nt = a.blocks * static_cast<int64_t>(kBlockCols * sizeof(T)) * (RES ? 3 : 2) > kStreamBytes;
   if (nt) hipLaunchKernelGGL((dropout_kernel<T, RES, true, U>), grid, dim3(kThreads), 0, st, a);
   else hipLaunchKernelGGL((dropout_kernel<T, RES, false, U>), grid, dim3(kThreads), 0, st, a);
 }

@@ -474,6 +474,15 @@ def test_dropout_many_blocks(Q):
         assert torch.equal(Q.Dropout(rows, cols, dtype, 0.25).run(x, 11 << 40, 1 << 50) != 0, keep)
 
 
+def test_gradient_rows_lie_as_the_logits_do(Q):
+    """A new gradient has every row at the same place within 16 bytes as the logits' row, at the least width."""
+    op = Q.PolicyLoss(4, 9, dtype="bf16")
+    lab, adv = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.ones(4, device="cuda")
+    for ld in (9, 10, 16, 17, 64):
+        g = op.run(torch.zeros(4, ld, dtype=torch.bfloat16, device="cuda")[:, :9], lab, adv)[2]
+        assert g.shape == (4, 9) and g.stride(1) == 1 and (g.stride(0) - ld) % 8 == 0 and 9 <= g.stride(0) <= 16
+
+
 # -- strides beyond 32 bits, streams, graphs, repeatability -----------------------------------
 
 def test_row_strides_past_32_bits(Q):

@@ -274,10 +274,17 @@ def test_run_refusals(lib):
     refused(A, drop.backward, x, 1, out=torch.zeros(4, 16)[:, ::2])
 
 
-def test_gradient_rows_lie_as_the_logits_do(lib):
-    """A new gradient has every row at the same place within 16 bytes as the logits' row."""
-    op = Q.PolicyLoss(4, 9, dtype="bf16", device="cpu")
-    for ld in (9, 10, 16, 17, 64):
-        x = torch.zeros(4, ld, dtype=torch.bfloat16)[:, :9]
-        g, gld = op._grad(x, op._matrix(x, "logits", 4, 9), None)
-        assert g.shape == (4, 9) and g.stride() == (gld, 1) and (gld - ld) % 8 == 0 and 9 <= gld <= 16
+def test_calls_that_are_not_tensors(lib):
+    """Anything but a tensor, and numbers that are not whole, are refused without a crash."""
+    x, lab = torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64)
+    op = Q.TokenLogp(4, 8, dtype="f32", device="cpu")
+    refused(K.KFAC_ERR_ARG, op.run, None, lab)
+    refused(K.KFAC_ERR_ARG, op.run, [1.0], lab)
+    refused(K.KFAC_ERR_ARG, op.run, x, "labels")
+    refused(K.KFAC_ERR_ARG, op.run, x.to_sparse(), lab)
+    drop = Q.Dropout(4, 8, dtype="f32", device="cpu")
+    with pytest.raises(TypeError):
+        drop.run(x, 1.5)
+    with pytest.raises(TypeError):
+        drop.run(x, 1, offset="two")
+    refused(K.KFAC_ERR_UNSUPPORTED, drop.run, x, -1, offset=1 << 70)      # taken modulo 2^64
