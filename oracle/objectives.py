@@ -91,7 +91,7 @@ def preference_terms(logp, labels, offsets, ref, weight, beta, kind, eps, averag
         h = seq[i] - seq[pairs + i]
         if kind == "sigmoid":
             x = beta * h
-            loss = (1 - eps) * np.logaddexp(0.0, -x) + eps * np.logaddexp(0.0, x)
+            loss = (1 - eps) * np.logaddexp(0.0, -x) + (eps * np.logaddexp(0.0, x) if eps else 0.0)
             slope = beta * (eps - 1.0 / (1.0 + np.exp(x)) if x >= 0 else 1.0 / (1.0 + np.exp(-x)) - (1.0 - eps))
         else:
             loss, slope = (h - 0.5 / beta) ** 2, 2.0 * (h - 0.5 / beta)

@@ -27,6 +27,8 @@ namespace {
 struct Plan {
   void* ws;
   size_t ws_bytes;
+  PyObject* ws_tensor;  // the tensor that holds the workspace, kept by the operator; NULL: none
+  void* home;           // the stream it was allocated on
   const char* name;
   int32_t device;
   int32_t dtype;
@@ -133,7 +135,10 @@ class Call {
     if (plan_.device < 0) refuse("the operators run on a GPU only", KFAC_ERR_UNSUPPORTED);
     guard_.emplace(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(plan_.device)));
     options_ = at::TensorOptions().device(c10::kCUDA, static_cast<c10::DeviceIndex>(plan_.device)).dtype(at::kFloat);
-    return c10::hip::getCurrentHIPStreamMasqueradingAsCUDA(static_cast<c10::DeviceIndex>(plan_.device)).stream();
+    const auto stream = c10::hip::getCurrentHIPStreamMasqueradingAsCUDA(static_cast<c10::DeviceIndex>(plan_.device));
+    // an operator may go while its call still runs elsewhere: the allocator then waits for that stream
+    if (plan_.ws_tensor && stream.stream() != plan_.home) THPVariable_Unpack(plan_.ws_tensor).record_stream(stream.unwrap());
+    return stream.stream();
   }
   at::Tensor make(int64_t n, at::ScalarType type = at::kFloat) const { return at::empty({n}, options_.dtype(type)); }
 

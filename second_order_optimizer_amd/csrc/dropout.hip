@@ -88,16 +88,9 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(DropArgs a) {
     const int64_t b = HALVES ? wave + (u / 2) * kThreads + (u & 1) * 32 + (lane >> 1) : first + u * kThreads + threadIdx.x;
     n[u] = 0;
     if (b < a.blocks) {
-      int64_t row;
-      uint32_t col;
-      if (a.blocks <= UINT32_MAX) {
-        const uint32_t q = static_cast<uint32_t>(b) / a.per_row;
-        row = q;
-        col = static_cast<uint32_t>(b) - q * a.per_row;
-      } else {
-        row = b / a.per_row;
-        col = static_cast<uint32_t>(b - row * a.per_row);
-      }
+      const uint32_t q = static_cast<uint32_t>(b) / a.per_row;      // at most kDropoutMaxBlocks in all
+      const uint32_t col = static_cast<uint32_t>(b) - q * a.per_row;
+      const int64_t row = q;
       const int lead = HALVES ? odd * VE : 0;
       const int64_t at = (static_cast<int64_t>(col) * kBlockCols + lead) * static_cast<int64_t>(sizeof(T));
       n[u] = col == a.per_row - 1 ? max(0, min(VE, static_cast<int>(a.tail) - lead)) : VE;

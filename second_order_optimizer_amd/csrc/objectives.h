@@ -10,6 +10,7 @@ namespace kfac {
 // Workspace regions behind the flag word, all 256-byte aligned.
 constexpr int kMaxPartials = 4096;        // policy: (A, K, clipped) sums, one triple per team of wavefronts
 constexpr int kBalanceMaxExperts = 1024;
+constexpr int64_t kDropoutMaxBlocks = (int64_t(1) << 32) - 1024;  // generator blocks a call
 constexpr int kBalanceBlocks = 512;       // balance: workgroups of the first pass
 
 size_t token_workspace_bytes(int objective, int64_t rows, int32_t groups);

@@ -171,8 +171,8 @@ kfac_status_t kfac_dropout(const kfac_dropout_t* d, void* stream) {
   if (!kfac::extent_ok(d->rows, d->ld) || !kfac::extent_ok(d->rows, d->y_ld) ||
       (d->residual && !kfac::extent_ok(d->rows, d->residual_ld)))
     return KFAC_ERR_UNSUPPORTED;
-  // one launch covers 2^31 workgroups; a row's blocks are counted in 32 bits
-  if (d->cols > INT32_MAX || (d->rows > 0 && (d->cols + 7) / 8 > (int64_t(1) << 39) / d->rows))
+  // one launch covers 2^32 - 1 threads, a thread one generator block of eight columns at least
+  if (d->rows > 0 && (d->cols > kfac::kDropoutMaxBlocks * 8 || (d->cols + 7) / 8 > kfac::kDropoutMaxBlocks / d->rows))
     return KFAC_ERR_UNSUPPORTED;
   if (d->rows == 0) return KFAC_OK;
   kfac::Ptrs p;

@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a
       lo[k] = hi[k] = 0;
     }
     double s = 0.0, n = 0.0;
-    for (int r = lo[k] + threadIdx.x; r < hi[k]; r += kPairThreads) {
+    for (int64_t r = lo[k] + static_cast<int64_t>(threadIdx.x); r < hi[k]; r += kPairThreads) {
       const int64_t l = load_index(a.labels, r, a.label_type);
       if (l < 0 || l >= a.vocab) continue;
       s += p.wide[r] - (p.ref ? static_cast<double>(p.ref[r]) : 0.0);
@@ -444,7 +444,8 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a
   double loss, slope;
   if (p.kind == KFAC_PREF_SIGMOID) {
     const double x = beta * h;
-    loss = (1.0 - eps) * softplus(-x) + eps * softplus(x);
+    loss = (1.0 - eps) * softplus(-x);
+    if (eps != 0.0) loss += eps * softplus(x);      // no 0 times infinity where x is infinite
     // sigma(x) - (1 - e), with sigma of the side that does not cancel
     const double sig = 1.0 / (1.0 + exp(fabs(x)));    // sigma(-|x|)
     slope = beta * (x >= 0.0 ? eps - sig : sig - (1.0 - eps));
@@ -465,7 +466,8 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a
   }
   for (int k = 0; k < 2; ++k) {
     const double f = w != 0.0 ? (k ? -w : w) * slope * share[k] * static_cast<double>(a.grad_scale) : 0.0;
-    for (int r = lo[k] + threadIdx.x; r < hi[k]; r += kPairThreads) {
+    if (threadIdx.x == 0 && !(fabsf(static_cast<float>(f)) < INFINITY)) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
+    for (int64_t r = lo[k] + static_cast<int64_t>(threadIdx.x); r < hi[k]; r += kPairThreads) {
       const int64_t l = load_index(a.labels, r, a.label_type);
       p.coef[r] = l >= 0 && l < a.vocab ? static_cast<float>(f) : 0.f;
     }

@@ -77,9 +77,9 @@ class DropoutArgs(ctypes.Structure):
 
 
 class _Plan(ctypes.Structure):
-    """Mirror of csrc/binding.cpp's Plan: workspace, device (-1: not a GPU), dtype."""
-    _fields_ = [("ws", _vp), ("ws_bytes", ctypes.c_size_t), ("name", ctypes.c_char_p), ("device", _i32),
-                ("dtype", _i32)]
+    """Mirror of csrc/binding.cpp's Plan: workspace, its tensor and stream, device (-1: not a GPU), dtype."""
+    _fields_ = [("ws", _vp), ("ws_bytes", ctypes.c_size_t), ("ws_tensor", _vp), ("home", _vp),
+                ("name", ctypes.c_char_p), ("device", _i32), ("dtype", _i32)]
 
 
 class _TokenPlan(ctypes.Structure):
@@ -160,15 +160,19 @@ class _Operator:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.dev = dev
         self.ws_ptr = self.ws_bytes = 0
+        tensor = home = None
         if objective is not None:
             self.ws_bytes = workspace_size(objective, rows, groups)
             self._ws = torch.zeros(self.ws_bytes + 256, dtype=torch.uint8, device=dev)
             self.ws_ptr = (self._ws.data_ptr() + 255) // 256 * 256
             if dev.type == "cuda":      # the workspace may be used on any stream from here on
-                torch.cuda.current_stream(dev).synchronize()
+                here = torch.cuda.current_stream(dev)
+                here.synchronize()
+                tensor, home = id(self._ws), here.cuda_stream
         self._plan = plan
         self._name = self._where.encode()
-        plan.base = _Plan(self.ws_ptr, self.ws_bytes, self._name, dev.index if dev.type == "cuda" else -1, self.code)
+        plan.base = _Plan(self.ws_ptr, self.ws_bytes, tensor, home, self._name,
+                          dev.index if dev.type == "cuda" else -1, self.code)
         self._at = ctypes.addressof(plan)
 
     def _fail(self, what: str, status: int = KFAC_ERR_ARG):

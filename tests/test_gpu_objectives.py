@@ -334,6 +334,33 @@ def test_preference(Q, vocab, dtype, kind, eps, average):
                      in_place=True, s=0.8)
 
 
+def test_preference_impossible_rejected_token(Q):
+    """A rejected sequence of probability 0: the pair is won outright, its loss and gradients are 0 without
+    smoothing; a preferred one of probability 0 is an infinite loss, which is flagged, with its gradient at the
+    limit, beta (p - onehot) on that side."""
+    x = torch.zeros(2, 8, device="cuda")
+    x[1, 3] = -float("inf")
+    lab = gpu([2, 3])
+    off = gpu([0, 1, 2], torch.int32)
+    op = Q.PreferenceLoss(2, 1, 8, "f32", beta=0.5)
+    stats, seq, logp, grad = op.run(x, lab, off)
+    assert stats[0] == 0 and stats[1] == 1 and stats[3] == 1 and seq[1] == -float("inf") and not grad.any()
+    assert op.flags(clear=True) == 0
+    stats, _, _, grad = op.run(x.flip(0).contiguous(), lab.flip(0).contiguous(), off)
+    assert stats[0] == float("inf") and op.flags() == 2
+    want = np.full(8, 0.5 / 7)
+    want[3] = -0.5
+    near(grad[0], want, 8 * U)
+    near(grad[1], np.where(np.arange(8) == 2, 0.5 * 7 / 8, -0.5 / 8), 8 * U)
+
+
+def test_preference_gradient_overflow_is_flagged(Q):
+    x = torch.zeros(2, 8, device="cuda")
+    op = Q.PreferenceLoss(2, 1, 8, "f32", beta=1e3, grad_scale=1e38)
+    stats = op.run(x, gpu([2, 3]), gpu([0, 1, 2], torch.int32))[0]
+    assert stats.isfinite().all() and op.flags() == 2
+
+
 def test_preference_many_rows(Q):
     check_preference(Q, np.random.default_rng(0), [400, 350, 600, 500, 300, 450], 513, "bf16", 0.1, "sigmoid", 0.1, False)
 
@@ -525,6 +552,27 @@ def test_another_stream(Q):
     torch.cuda.current_stream().wait_stream(s)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     assert torch.equal(y, Q.Dropout(300, 5000, "f32").run(x, 1))
+
+
+def test_workspace_outlives_its_object_on_another_stream(Q):
+    """An operator dropped while its call still runs on another stream: its workspace is not handed out again
+    before that call has ended."""
+    s = torch.cuda.Stream()
+    x = torch.randn(2000, 30000, device="cuda")
+    lab, off = torch.randint(0, 30000, (2000,), device="cuda"), gpu([0, 1000, 2000], torch.int32)
+    want = Q.PreferenceLoss(2000, 1, 30000, "f32").run(x, lab, off)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        op = Q.PreferenceLoss(2000, 1, 30000, "f32")
+        n = op.ws_bytes + 256
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got = op.run(x, lab, off)
+        del op
+        spoiled = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.current_stream().wait_stream(s)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        del spoiled
 
 
 def test_graph_replays(Q):

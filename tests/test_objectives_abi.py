@@ -199,6 +199,13 @@ def test_dropout_refusals(lib, bad, code):
     assert lib.kfac_dropout(None, None) == K.KFAC_ERR_ARG
 
 
+def test_dropout_past_one_launch_is_refused(lib):
+    """More than 2^32 - 1024 generator blocks (2^35 elements) do not fit a launch's count of threads."""
+    for r, cols in ((1 << 32, 8), (1 << 20, 1 << 15), (1, 1 << 36), ((1 << 32) - 1023, 1)):
+        d = dropout(rows=r, cols=cols, ld=cols, residual_ld=cols, y_ld=cols)
+        assert lib.kfac_dropout(ctypes.byref(d), None) == K.KFAC_ERR_UNSUPPORTED, (r, cols)
+
+
 def test_dropout_of_nothing(lib):
     """No rows: nothing to do, no pointers needed, no launch."""
     d = dropout(rows=0, x=None, y=None, residual=None)
