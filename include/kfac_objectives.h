@@ -11,8 +11,8 @@
  *
  * Conventions, as in kfac.h: device pointers owned by the caller, `stream` a
  * hipStream_t the calls only enqueue on, `workspace` 256-byte aligned with a
- * sticky flag word at its start that the caller zeroes once (kfac_read_flags
- * reads it), one workspace for one call at a time; arguments are validated
+ * sticky flag word at its start (kfac_read_flags reads it), zeroed whole
+ * once by the caller, one workspace for one call at a time; arguments are validated
  * before anything is enqueued.  Differences: matrices are row-major with a
  * row stride in elements (`ld` >= the width), and a pointer needs the
  * alignment of its element type only.  Nothing is allocated and no host

@@ -20,8 +20,13 @@
 // has out of the sums; both compute the same gradient there.  E below a vector:
 // one element a lane.
 //
-// Bound by vector arithmetic and the lane reductions, not by memory: some 14
-// operations an element and pass, the exponential counting four.
+// 65536 tokens of 256 bf16 logits: first pass 13.8 us (arithmetic, some 14
+// operations an element with the exponential counting four, and the memory's
+// latency at either end: four tokens a lane in all), sums 4.6 us (latency),
+// second pass 16.5 us (67 MB through the cache at 4.1 TB/s).  The next token's
+// logits are loaded while one is worked on, and 8 wavefronts fit a SIMD.  With
+// workgroups of 512, the mask waited for before the logits and the softmax
+// found twice it was 15.5, 4.6 and 22 us.
 #include "objectives.h"
 
 #include <algorithm>
@@ -30,10 +35,10 @@ namespace kfac {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kSmallThreads = 1024;
+constexpr int kThreads = 1024;
+constexpr int kGradThreads = 256, kGradBlocks = 2048;
 constexpr int kSmallRounds = 8;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct BalArgs {
   const char* x;
@@ -54,6 +59,8 @@ struct BalArgs {
   double* part_z;        // [blocks]
   int32_t* part_n;       // [blocks]
   double* prob64;        // [E]
+  float* f;              // [E]: a count's weight in the gradient
+  float2* stat;          // [tokens]: (maximum, 1 / sum), the latter 0 for a token that does not count
   double* total;         // [2]: n, sum of lse^2
 };
 
@@ -93,7 +100,7 @@ struct Shape {
   static constexpr bool EVEN = EVEN_;
   static constexpr int SLOTS = kWave / LPT;      // tokens a wavefront
   static constexpr int W = LPT * NV * VEC;       // columns at most
-  static constexpr int U = NV == 1 ? 2 : 1;      // tokens a lane works on at once
+  static constexpr int WAVES = NV == 1 ? 8 : 4;  // wavefronts a SIMD that the registers have to leave room for
 };
 
 // Where a lane's vectors lie in a row, and how many of their first columns
@@ -118,31 +125,53 @@ struct Columns {
   }
 };
 
-__device__ inline bool token_live(const BalArgs& a, int64_t t) {
-  return t < a.tokens && (!a.mask || a.mask[t] != 0);
-}
-
-// A token's logits (zeros for one that does not count: it is not looked at),
-// minus infinity past the row.
+// A lane's part of a token's logits, minus infinity past the row.
 template <typename S>
-__device__ inline void load_token(float (&x)[S::NV][S::VEC], const BalArgs& a, int64_t t, bool live,
-                                  const Columns<S>& cols) {
+__device__ inline void load_row(u32x4 (&v)[S::NV], const BalArgs& a, int64_t t, const Columns<S>& cols) {
   using T = typename S::T;
   const char* row = a.x + t * a.ldx;
 #pragma unroll
   for (int q = 0; q < S::NV; ++q) {
-#pragma unroll
-    for (int i = 0; i < S::VEC; ++i) x[q][i] = live ? -INFINITY : 0.f;
-    if (live && cols.skip[q] < S::VEC) {
-      if constexpr (S::VEC == 1) {
-        x[q][0] = Elem<T>::load(row, cols.col[q]);
-      } else {
-        const u32x4 v = load16(row + static_cast<int64_t>(cols.col[q]) * sizeof(T));
-#pragma unroll
-        for (int i = 0; i < S::VEC; ++i) x[q][i] = Elem<T>::get(v, i);
-      }
+    v[q] = u32x4{Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf};
+    if (cols.skip[q] < S::VEC) {
+      if constexpr (S::VEC > 1) v[q] = load16(row + static_cast<int64_t>(cols.col[q]) * sizeof(T));
+      else if constexpr (sizeof(T) == 2) v[q][0] = reinterpret_cast<const unsigned short*>(row)[cols.col[q]];
+      else v[q][0] = reinterpret_cast<const uint32_t*>(row)[cols.col[q]];
     }
   }
+}
+
+// A token's logits as they are loaded.  A token that is masked out is loaded
+// too, so that its mask and its logits are waited for together, and counts as
+// zeros from there on.
+template <typename S>
+struct TokenIn {
+  u32x4 v[S::NV];
+  uint8_t live;
+
+  __device__ void load(const BalArgs& a, int64_t t, const Columns<S>& cols) {
+#pragma unroll
+    for (int q = 0; q < S::NV; ++q) v[q] = u32x4{0u, 0u, 0u, 0u};
+    live = 0;
+    if (t >= a.tokens) return;
+    load_row<S>(v, a, t, cols);
+    live = a.mask ? a.mask[t] : 1;
+  }
+  // The logits, minus infinity past the row; zeros for a token that does not count.
+  __device__ void expand(float (&x)[S::NV][S::VEC]) const {
+#pragma unroll
+    for (int q = 0; q < S::NV; ++q) {
+      const u32x4 w = live ? v[q] : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int i = 0; i < S::VEC; ++i) x[q][i] = Elem<typename S::T>::get(w, i);
+    }
+  }
+};
+
+// 1 / s of a sum of exponentials (1 .. 1024), to float32's width.
+__device__ inline float inverse(float s) {
+  const float r = __builtin_amdgcn_rcpf(s);
+  return fmaf(fmaf(-s, r, 1.f), r, r);
 }
 
 template <typename S>
@@ -156,67 +185,90 @@ __device__ inline float row_maximum(const float (&x)[S::NV][S::VEC]) {
   return group_reduce<S::LPT, true>(m);
 }
 
-// First pass over a wavefront's tokens t0 + slot, t0 + stride + slot, ...:
-// adds p to the lane's columns, lse^2 and the tokens that count (in a token's
-// first lane).
+// First pass over a wavefront's tokens t0 + slot, t0 + stride + slot, ..., the
+// first of which is loaded: adds p to the lane's columns, lse^2 and the tokens
+// that count (in a token's first lane); keeps each token's maximum and 1 / sum.
 template <typename S>
 __device__ inline void count_tokens(const BalArgs& a, const Columns<S>& cols, int64_t t0, int64_t stride,
-                                    float (&acc)[S::NV][S::VEC], double& z, int& n) {
-  constexpr int U = S::U;
+                                    TokenIn<S> in, float (&acc)[S::NV][S::VEC], double& z, int& n) {
   const int lane = threadIdx.x & (kWave - 1), slot = lane / S::LPT, sub = lane % S::LPT;
-  for (; t0 < a.tokens; t0 += stride * U) {
-    float x[U][S::NV][S::VEC];
-    bool live[U];
+  for (; t0 < a.tokens; t0 += stride) {
+    const int64_t t = t0 + slot;
+    float x[S::NV][S::VEC];
+    const bool live = in.live != 0;
+    in.expand(x);
+    in.load(a, t + stride, cols);
+    if constexpr (!S::EVEN) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t t = t0 + u * stride + slot;
-      live[u] = token_live(a, t);
-      load_token<S>(x[u], a, t, live[u], cols);
+      for (int q = 0; q < S::NV; ++q)
+#pragma unroll
+        for (int i = 0; i < S::VEC; ++i) x[q][i] = i < cols.skip[q] ? -INFINITY : x[q][i];
     }
+    const float m = row_maximum<S>(x);
+    float s = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if constexpr (!S::EVEN) {
+    for (int q = 0; q < S::NV; ++q)
 #pragma unroll
-        for (int q = 0; q < S::NV; ++q)
-#pragma unroll
-          for (int i = 0; i < S::VEC; ++i) x[u][q][i] = i < cols.skip[q] ? -INFINITY : x[u][q][i];
+      for (int i = 0; i < S::VEC; ++i) {
+        x[q][i] = __builtin_amdgcn_exp2f((x[q][i] - m) * kLog2e);
+        s += x[q][i];
       }
-      const float m = row_maximum<S>(x[u]);
-      float s = 0.f;
+    s = group_reduce<S::LPT, false>(s);
+    const float inv = live ? inverse(s) : 0.f;
+    if (sub == 0 && t < a.tokens) a.stat[t] = make_float2(m, inv);
 #pragma unroll
-      for (int q = 0; q < S::NV; ++q)
+    for (int q = 0; q < S::NV; ++q)
 #pragma unroll
-        for (int i = 0; i < S::VEC; ++i) {
-          x[u][q][i] = __builtin_amdgcn_exp2f((x[u][q][i] - m) * kLog2e);
-          s += x[u][q][i];
-        }
-      s = group_reduce<S::LPT, false>(s);
-      const float inv = live[u] ? 1.f / s : 0.f;
-#pragma unroll
-      for (int q = 0; q < S::NV; ++q)
-#pragma unroll
-        for (int i = 0; i < S::VEC; ++i) acc[q][i] = fmaf(x[u][q][i], inv, acc[q][i]);
-      const bool first = live[u] && sub == 0;
-      const float lse = first ? m + logf(s) : 0.f;
+      for (int i = 0; i < S::VEC; ++i) acc[q][i] = fmaf(x[q][i], inv, acc[q][i]);
+    const bool first = live && sub == 0;
+    if (a.z != 0.f) {
+      const float lse = first ? fmaf(__builtin_amdgcn_logf(s), kLn2, m) : 0.f;
       z += static_cast<double>(lse) * static_cast<double>(lse);
-      n += first;
     }
+    n += first;
   }
 }
 
 // Histogram of the chosen experts, from thread `first` of `threads`: integer
-// counts, in any order.
-__device__ inline void count_chosen(const BalArgs& a, int* hist, int64_t first, int64_t threads) {
-  const int64_t slots = a.tokens * a.k;
-  for (int64_t i = first; i < slots; i += threads) {
-    const int64_t t = slots <= INT32_MAX ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(a.k))
-                                         : i / a.k;
-    if (!token_live(a, t)) continue;
-    const int64_t e = load_index(a.chosen, i, a.index_type);
+// counts, in any order.  The first kAhead slots of a thread are loaded before
+// the histogram is cleared.
+constexpr int kAhead = 2;
+struct Chosen {
+  int64_t e[kAhead];
+  uint8_t live[kAhead];
+
+  static __device__ int64_t token(const BalArgs& a, int64_t i) {
+    return a.tokens * a.k <= INT32_MAX
+               ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(a.k)) : i / a.k;
+  }
+  static __device__ void add(const BalArgs& a, int* hist, int64_t e) {
     if (e >= a.E) raise_flag(a.flags, KFAC_FLAG_BAD_INDEX);
     else if (e >= 0) atomicAdd(&hist[e], 1);
   }
-}
+  __device__ void load(const BalArgs& a, int64_t first, int64_t threads) {
+    const int64_t slots = a.tokens * a.k;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t i = first + j * threads;
+      live[j] = 0;
+      e[j] = -1;
+      if (i < slots) {
+        e[j] = load_index(a.chosen, i, a.index_type);
+        live[j] = a.mask ? a.mask[token(a, i)] : 1;
+      }
+    }
+  }
+  __device__ void count(const BalArgs& a, int* hist, int64_t first, int64_t threads) const {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (live[j]) add(a, hist, e[j]);
+    const int64_t slots = a.tokens * a.k;
+    for (int64_t i = first + kAhead * threads; i < slots; i += threads) {
+      const int64_t c = load_index(a.chosen, i, a.index_type);
+      if (!a.mask || a.mask[token(a, i)] != 0) add(a, hist, c);
+    }
+  }
+};
 
 // A wavefront's column sums, over its slots, into psum[0 .. E): each column
 // from the lane it belongs to.
@@ -232,53 +284,56 @@ __device__ inline void column_sums(const Columns<S>& cols, const float (&acc)[S:
     }
 }
 
-// Second pass: the gradients, from f of the lane's columns and zs = 2 z_coef /
-// n (both times grad_scale).
+// Second pass: the gradients, from each token's maximum and inverse sum as the
+// first pass found them (a third less arithmetic than to find them again:
+// 65536 x 256 bf16 22 -> 16.5 us with the loads ahead), from f of the lane's
+// columns and zs = 2 z_coef / n (both times grad_scale).
+template <typename S>
+struct TokenBack {
+  u32x4 v[S::NV];
+  float2 stat;
+
+  __device__ void load(const BalArgs& a, int64_t t, const Columns<S>& cols) {
+#pragma unroll
+    for (int q = 0; q < S::NV; ++q) v[q] = u32x4{0u, 0u, 0u, 0u};
+    stat = make_float2(0.f, 0.f);
+    if (t >= a.tokens) return;
+    load_row<S>(v, a, t, cols);
+    stat = a.stat[t];
+  }
+};
+
 template <typename S>
 __device__ inline void grad_tokens(const BalArgs& a, const Columns<S>& cols, int64_t t0, int64_t stride,
-                                   const float (&f)[S::NV][S::VEC], float zs) {
+                                   TokenBack<S> in, const float (&f)[S::NV][S::VEC], float zs) {
   using T = typename S::T;
-  constexpr int U = S::U;
   const int slot = (threadIdx.x & (kWave - 1)) / S::LPT;
-  for (; t0 < a.tokens; t0 += stride * U) {
-    float x[U][S::NV][S::VEC];
-    bool live[U];
+  for (; t0 < a.tokens; t0 += stride) {
+    const int64_t t = t0 + slot;
+    const TokenBack<S> cur = in;
+    in.load(a, t + stride, cols);
+    const float m = cur.stat.x, inv = cur.stat.y;
+    float p[S::NV][S::VEC], pf = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t t = t0 + u * stride + slot;
-      live[u] = token_live(a, t);
-      load_token<S>(x[u], a, t, live[u], cols);
-    }
+    for (int q = 0; q < S::NV; ++q)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t t = t0 + u * stride + slot;
-      const float m = row_maximum<S>(x[u]);
-      float s = 0.f, pf = 0.f;
+      for (int i = 0; i < S::VEC; ++i) {
+        p[q][i] = __builtin_amdgcn_exp2f((Elem<T>::get(cur.v[q], i) - m) * kLog2e) * inv;
+        pf = fmaf(S::EVEN || i >= cols.skip[q] ? p[q][i] : 0.f, f[q][i], pf);
+      }
+    pf = group_reduce<S::LPT, false>(pf);
+    const bool live = inv != 0.f;
+    const float shift = (zs != 0.f ? zs * fmaf(__builtin_amdgcn_logf(inv), -kLn2, m) : 0.f) - pf;
+    if (t >= a.tokens) continue;
+    char* row = a.g + t * a.ldg;
 #pragma unroll
-      for (int q = 0; q < S::NV; ++q)
+    for (int q = 0; q < S::NV; ++q) {
+      if (cols.skip[q] < S::VEC) {
+        float g[S::VEC];
 #pragma unroll
-        for (int i = 0; i < S::VEC; ++i) {
-          x[u][q][i] = __builtin_amdgcn_exp2f((x[u][q][i] - m) * kLog2e);
-          const float e = S::EVEN || i >= cols.skip[q] ? x[u][q][i] : 0.f;
-          s += e;
-          pf = fmaf(e, f[q][i], pf);
-        }
-      s = group_reduce<S::LPT, false>(s);
-      pf = group_reduce<S::LPT, false>(pf);
-      const float inv = live[u] ? 1.f / s : 0.f;
-      const float shift = (zs != 0.f ? zs * (m + logf(s)) : 0.f) - pf * inv;
-      if (t < a.tokens) {
-        char* row = a.g + t * a.ldg;
-#pragma unroll
-        for (int q = 0; q < S::NV; ++q) {
-          if (cols.skip[q] < S::VEC) {
-            float g[S::VEC];
-#pragma unroll
-            for (int i = 0; i < S::VEC; ++i) g[i] = x[u][q][i] * inv * (f[q][i] + shift);
-            if constexpr (S::VEC == 1) Elem<T>::store(row, cols.col[q], g[0]);
-            else store16(row + static_cast<int64_t>(cols.col[q]) * sizeof(T), pack16<T>(g));
-          }
-        }
+        for (int i = 0; i < S::VEC; ++i) g[i] = p[q][i] * (f[q][i] + shift);
+        if constexpr (S::VEC == 1) Elem<T>::store(row, cols.col[q], live ? g[0] : 0.f);
+        else store16(row + static_cast<int64_t>(cols.col[q]) * sizeof(T), live ? pack16<T>(g) : u32x4{0u, 0u, 0u, 0u});
       }
     }
   }
@@ -304,9 +359,9 @@ struct Scales {
   }
 };
 
-template <typename S, int THREADS>
+template <typename S>
 struct CountShared {
-  static constexpr int WAVES = THREADS / kWave;
+  static constexpr int WAVES = kThreads / kWave;
   int hist[S::W];
   float psum[WAVES][S::W];
   double z[WAVES];
@@ -315,14 +370,20 @@ struct CountShared {
   // Everything of the first pass for this workgroup: hist, psum, z and n.
   __device__ void count(const BalArgs& a, const Columns<S>& cols, int block, int blocks) {
     const int wid = threadIdx.x / kWave;
-    for (int e = threadIdx.x; e < a.E; e += THREADS) hist[e] = 0;
+    const int64_t per = static_cast<int64_t>(WAVES) * S::SLOTS, t0 = block * per + wid * S::SLOTS, stride = blocks * per;
+    const int64_t first = static_cast<int64_t>(block) * kThreads + threadIdx.x;
+    const int64_t threads = static_cast<int64_t>(blocks) * kThreads;
+    TokenIn<S> in;
+    in.load(a, t0 + (threadIdx.x & (kWave - 1)) / S::LPT, cols);
+    Chosen chosen;
+    chosen.load(a, first, threads);
+    for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
     __syncthreads();
     float acc[S::NV][S::VEC] = {};
     double zs = 0.0;
     int ns = 0;
-    const int64_t per = static_cast<int64_t>(WAVES) * S::SLOTS;
-    count_tokens<S>(a, cols, block * per + wid * S::SLOTS, blocks * per, acc, zs, ns);
-    count_chosen(a, hist, static_cast<int64_t>(block) * THREADS + threadIdx.x, static_cast<int64_t>(blocks) * THREADS);
+    count_tokens<S>(a, cols, t0, stride, in, acc, zs, ns);
+    chosen.count(a, hist, first, threads);
     column_sums<S>(cols, acc, psum[wid]);
     zs = wave_sum(zs);
     ns = slot_sum<1>(ns);
@@ -350,8 +411,8 @@ struct CountShared {
 };
 
 template <typename S>
-__global__ void __launch_bounds__(kThreads) balance_count_kernel(BalArgs a) {
-  __shared__ CountShared<S, kThreads> sh;
+__global__ void __launch_bounds__(kThreads, S::WAVES) balance_count_kernel(BalArgs a) {
+  __shared__ CountShared<S> sh;
   const Columns<S> cols(threadIdx.x % S::LPT, a.E);
   sh.count(a, cols, blockIdx.x, gridDim.x);
   const int64_t at = static_cast<int64_t>(blockIdx.x) * a.E;
@@ -412,6 +473,7 @@ __global__ void __launch_bounds__(1024) balance_reduce_kernel(BalArgs a) {
       a.prob[e] = static_cast<float>(s);
       a.prob64[e] = s;
       a.counts[e] = t;
+      a.f[e] = static_cast<float>(Scales(a, n).unit(a) * t);
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       a.total[0] = n;
@@ -421,9 +483,18 @@ __global__ void __launch_bounds__(1024) balance_reduce_kernel(BalArgs a) {
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kThreads) balance_grad_kernel(BalArgs a) {
+__global__ void __launch_bounds__(kGradThreads, S::WAVES) balance_grad_kernel(BalArgs a) {
   const int lane = threadIdx.x & (kWave - 1), wid = threadIdx.x / kWave;
   const Columns<S> cols(lane % S::LPT, a.E);
+  const int64_t per = static_cast<int64_t>(kGradThreads / kWave) * S::SLOTS;
+  const int64_t t0 = blockIdx.x * per + wid * S::SLOTS, stride = gridDim.x * per;
+  TokenBack<S> in;
+  in.load(a, t0 + lane / S::LPT, cols);
+  float f[S::NV][S::VEC];
+#pragma unroll
+  for (int q = 0; q < S::NV; ++q)
+#pragma unroll
+    for (int i = 0; i < S::VEC; ++i) f[q][i] = cols.skip[q] < S::VEC ? a.f[cols.col[q] + i] : 0.f;
   const double live = a.total[0];
   const Scales sc(a, live);
   if (blockIdx.x == 0 && wid == 0) {
@@ -432,21 +503,13 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(BalArgs a) {
     dot = wave_sum(dot);
     if (lane == 0) sc.write(a, dot, a.total[1], live);
   }
-  const double unit = sc.unit(a);
-  float f[S::NV][S::VEC];
-#pragma unroll
-  for (int q = 0; q < S::NV; ++q)
-#pragma unroll
-    for (int i = 0; i < S::VEC; ++i)
-      f[q][i] = cols.skip[q] < S::VEC ? static_cast<float>(unit * a.counts[cols.col[q] + i]) : 0.f;
-  const int64_t per = static_cast<int64_t>(kThreads / kWave) * S::SLOTS;
-  grad_tokens<S>(a, cols, blockIdx.x * per + wid * S::SLOTS, gridDim.x * per, f, sc.zs(a));
+  grad_tokens<S>(a, cols, t0, stride, in, f, sc.zs(a));
 }
 
 // All of it in one workgroup, for a few tokens.
 template <typename S>
-__global__ void __launch_bounds__(kSmallThreads) balance_small_kernel(BalArgs a) {
-  using Shared = CountShared<S, kSmallThreads>;
+__global__ void __launch_bounds__(kThreads) balance_small_kernel(BalArgs a) {
+  using Shared = CountShared<S>;
   __shared__ Shared sh;
   __shared__ double dots[Shared::WAVES];
   const int lane = threadIdx.x & (kWave - 1), wid = threadIdx.x / kWave;
@@ -455,7 +518,7 @@ __global__ void __launch_bounds__(kSmallThreads) balance_small_kernel(BalArgs a)
   const double live = sh.n_sum();
   const Scales sc(a, live);
   double dot = 0.0;
-  for (int e = threadIdx.x; e < a.E; e += kSmallThreads) {
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
     const double p = sh.column(e) / sc.n;
     a.prob[e] = static_cast<float>(p);
     a.counts[e] = sh.hist[e];
@@ -477,13 +540,15 @@ __global__ void __launch_bounds__(kSmallThreads) balance_small_kernel(BalArgs a)
     for (int i = 0; i < S::VEC; ++i)
       f[q][i] = cols.skip[q] < S::VEC ? static_cast<float>(unit * sh.hist[cols.col[q] + i]) : 0.f;
   const int64_t per = static_cast<int64_t>(Shared::WAVES) * S::SLOTS;
-  grad_tokens<S>(a, cols, wid * S::SLOTS, per, f, sc.zs(a));
+  TokenBack<S> in;
+  in.load(a, wid * S::SLOTS + lane / S::LPT, cols);
+  grad_tokens<S>(a, cols, wid * S::SLOTS, per, in, f, sc.zs(a));
 }
 
 template <typename S>
 kfac_status_t run(BalArgs a, hipStream_t st) {
-  if (a.tokens <= static_cast<int64_t>(kSmallRounds) * (kSmallThreads / S::LPT)) {
-    hipLaunchKernelGGL((balance_small_kernel<S>), dim3(1), dim3(kSmallThreads), 0, st, a);
+  if (a.tokens <= static_cast<int64_t>(kSmallRounds) * (kThreads / S::LPT)) {
+    hipLaunchKernelGGL((balance_small_kernel<S>), dim3(1), dim3(kThreads), 0, st, a);
     KFAC_HIP_TRY(hipGetLastError());
     return KFAC_OK;
   }
@@ -494,8 +559,9 @@ kfac_status_t run(BalArgs a, hipStream_t st) {
   KFAC_HIP_TRY(hipGetLastError());
   hipLaunchKernelGGL(balance_reduce_kernel, dim3((a.E + 15) / 16), dim3(1024), 0, st, a);
   KFAC_HIP_TRY(hipGetLastError());
-  hipLaunchKernelGGL((balance_grad_kernel<S>), dim3(static_cast<int>(std::min<int64_t>(need, 1024))), dim3(kThreads), 0,
-                     st, a);
+  const int64_t grad_need = need * (kThreads / kGradThreads);
+  hipLaunchKernelGGL((balance_grad_kernel<S>), dim3(static_cast<int>(std::min<int64_t>(grad_need, kGradBlocks))),
+                     dim3(kGradThreads), 0, st, a);
   KFAC_HIP_TRY(hipGetLastError());
   return KFAC_OK;
 }
@@ -525,26 +591,28 @@ kfac_status_t pick(const BalArgs& a, hipStream_t st) {
 }
 
 struct Regions {
-  size_t p, c, z, n, prob, total, end;
+  size_t p, c, z, n, prob, f, stat, total, end;
 };
-Regions regions(int32_t E) {
+Regions regions(int64_t tokens, int32_t E) {
   Regions r;
   r.p = kFlagBytes;
   r.c = r.p + align_up(sizeof(float) * kBalanceBlocks * static_cast<size_t>(E), 256);
   r.z = r.c + align_up(sizeof(int32_t) * kBalanceBlocks * static_cast<size_t>(E), 256);
   r.n = r.z + align_up(sizeof(double) * kBalanceBlocks, 256);
   r.prob = r.n + align_up(sizeof(int32_t) * kBalanceBlocks, 256);
-  r.total = r.prob + align_up(sizeof(double) * static_cast<size_t>(E), 256);
+  r.f = r.prob + align_up(sizeof(double) * static_cast<size_t>(E), 256);
+  r.stat = r.f + align_up(sizeof(float) * static_cast<size_t>(E), 256);
+  r.total = r.stat + align_up(sizeof(float2) * static_cast<size_t>(tokens), 256);
   r.end = r.total + 256;
   return r;
 }
 
 }  // namespace
 
-size_t balance_workspace_bytes(int32_t experts) { return regions(experts).end; }
+size_t balance_workspace_bytes(int64_t tokens, int32_t experts) { return regions(tokens, experts).end; }
 
 kfac_status_t launch_balance(const kfac_balance_t& b, char* ws, hipStream_t st) {
-  const Regions r = regions(b.experts);
+  const Regions r = regions(b.tokens, b.experts);
   const int64_t el = b.dtype == KFAC_BF16 ? 2 : 4;
   BalArgs a{};
   a.x = static_cast<const char*>(b.logits);
@@ -569,6 +637,8 @@ kfac_status_t launch_balance(const kfac_balance_t& b, char* ws, hipStream_t st) 
   a.part_z = reinterpret_cast<double*>(ws + r.z);
   a.part_n = reinterpret_cast<int32_t*>(ws + r.n);
   a.prob64 = reinterpret_cast<double*>(ws + r.prob);
+  a.f = reinterpret_cast<float*>(ws + r.f);
+  a.stat = reinterpret_cast<float2*>(ws + r.stat);
   a.total = reinterpret_cast<double*>(ws + r.total);
   return b.dtype == KFAC_BF16 ? pick<__bf16>(a, st) : pick<float>(a, st);
 }

@@ -8,13 +8,13 @@
 namespace kfac {
 
 // Workspace regions behind the flag word, all 256-byte aligned.
-constexpr int kMaxPartials = 4096;        // policy: (A, K, clipped) sums, one triple per team of wavefronts
+constexpr int kMaxPartials = 2048;        // policy: (A, K, clipped) sums, one triple a workgroup
 constexpr int kBalanceMaxExperts = 1024;
 constexpr int64_t kDropoutMaxBlocks = (int64_t(1) << 32) - 1024;  // generator blocks a call
 constexpr int kBalanceBlocks = 512;       // balance: workgroups of the first pass
 
 size_t token_workspace_bytes(int objective, int64_t rows, int32_t groups);
-size_t balance_workspace_bytes(int32_t experts);
+size_t balance_workspace_bytes(int64_t tokens, int32_t experts);
 
 kfac_status_t launch_token_logp(const kfac_token_rows_t& t, char* ws, hipStream_t st);
 kfac_status_t launch_policy(const kfac_token_rows_t& t, const kfac_policy_t& p, char* ws, hipStream_t st);

@@ -72,7 +72,8 @@ kfac_status_t kfac_objective_workspace_size(int32_t objective, int64_t rows, int
     case KFAC_OBJ_BALANCE:
       if (groups < 1) return KFAC_ERR_ARG;
       if (groups > kfac::kBalanceMaxExperts) return KFAC_ERR_UNSUPPORTED;
-      *bytes = kfac::balance_workspace_bytes(groups);
+      if (rows > INT32_MAX) return KFAC_ERR_UNSUPPORTED;
+      *bytes = kfac::balance_workspace_bytes(rows, groups);
       return KFAC_OK;
     default: return KFAC_ERR_ARG;
   }
@@ -155,7 +156,7 @@ kfac_status_t kfac_balance_loss(const kfac_balance_t* b, void* workspace, size_t
     p.need(b->chosen, kfac::index_size(b->index_type));
   }
   if (p.s != KFAC_OK) return p.s;
-  kfac_status_t s = kfac::check_workspace(workspace, ws_bytes, kfac::balance_workspace_bytes(b->experts));
+  kfac_status_t s = kfac::check_workspace(workspace, ws_bytes, kfac::balance_workspace_bytes(b->tokens, b->experts));
   if (s != KFAC_OK) return s;
   return kfac::launch_balance(*b, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
 }

@@ -42,7 +42,9 @@ struct TokArgs {
 
 struct PolArgs {
   const float *adv, *weight, *old_logp, *ref;
-  double* part;        // [gridDim.x][3]
+  uint64_t* part;      // [gridDim.x][3] doubles
+  uint32_t* arrived;   // counters of workgroups that are done, 0 between calls
+  float* stats;
   float lo, hi, kl;
   float w0;            // weight where none is given
 };
@@ -59,7 +61,9 @@ struct Softmax {
 // FINE multiplies by s log2(e) to twice float32's width: c alone is off by up
 // to 3e-8 of itself, which biases log S by that times the mean exponent, the
 // same way in every row; sums of log-probabilities over a sequence would show
-// it.  The gradients do without.
+// it.  bf16 gradients do without.
+template <typename T>
+constexpr bool kFine = sizeof(T) == 4;
 template <bool FINE>
 __device__ inline float exp_of(float d, float c, float clo) {
   return __builtin_amdgcn_exp2f(FINE ? fmaf(d, c, d * clo) : d * c);
@@ -119,7 +123,8 @@ __device__ inline Softmax team_softmax(Softmax a, float c, Softmax* red, int par
 }
 
 __device__ inline float log_prob(float xl, Softmax r, float scale) {
-  return (xl - r.m) * scale - logf(static_cast<float>(r.s));
+  const float s = static_cast<float>(r.s);
+  return (xl - r.m) * scale - (logf(s) + static_cast<float>(r.s - static_cast<double>(s)) / s);
 }
 
 // The label of a row, -1 for one to leave out (a label beyond the vocabulary
@@ -135,15 +140,15 @@ __device__ inline int32_t row_label(const TokArgs& a, int64_t row) {
 
 // coef / S times exp(s (x - M)), negated and rounded: a vector of the gradient.
 template <typename T>
-__device__ inline u32x4 grad_vec(u32x4 v, float m, float c, float neg) {
+__device__ inline u32x4 grad_vec(u32x4 v, float m, float c, float clo, float neg) {
   float o[Elem<T>::VE];
 #pragma unroll
-  for (int i = 0; i < Elem<T>::VE; ++i) o[i] = __builtin_amdgcn_exp2f((Elem<T>::get(v, i) - m) * c) * neg;
+  for (int i = 0; i < Elem<T>::VE; ++i) o[i] = exp_of<kFine<T>>(Elem<T>::get(v, i) - m, c, clo) * neg;
   return pack16<T>(o);
 }
 template <typename T>
-__device__ inline float grad_one(float x, float m, float c, float neg) {
-  return __builtin_amdgcn_exp2f((x - m) * c) * neg;
+__device__ inline float grad_one(float x, float m, float c, float clo, float neg) {
+  return exp_of<kFine<T>>(x - m, c, clo) * neg;
 }
 
 // ---------------------------------------------------------------------------
@@ -171,6 +176,62 @@ __device__ inline RowScalars row_scalars(const TokArgs& a, const PolArgs& p, int
   return r;
 }
 
+// stats from the workgroups' sums: the workgroup that counts itself last adds
+// them up, in a fixed order, and leaves the counters at 0 for the next call.
+// Workgroups count in groups of kArriveGroup, the last of a group counts it: on
+// one counter 1536 workgroups took 18 us.  The sums are stored and loaded at
+// device scope, past the XCDs' own caches, and counted once the stores have
+// arrived, so no cache has to be written back (a release fence in every
+// workgroup does that: 2047 x 50001 bf16 92 -> 103 us).  A kernel of its own
+// for these sums took 4 us and a launch.
+constexpr int kArriveGroup = 32, kArriveStride = 64;      // counters 256 bytes apart
+
+__device__ inline bool counted_last(uint32_t* counter, uint32_t of) {
+  if (__hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != of - 1) return false;
+  __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return true;
+}
+
+template <int TEAMS>
+__device__ inline void policy_stats(const PolArgs& p, const double (*sums)[3], int* last) {
+  if (threadIdx.x == 0) {
+    uint64_t* q = p.part + static_cast<int64_t>(blockIdx.x) * 3;
+    for (int k = 0; k < 3; ++k) {
+      double t = 0.0;
+      for (int i = 0; i < TEAMS; ++i) t += sums[i][k];
+      __hip_atomic_store(q + k, __builtin_bit_cast(uint64_t, t), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const uint32_t group = blockIdx.x / kArriveGroup, groups = (gridDim.x + kArriveGroup - 1) / kArriveGroup;
+    const uint32_t size = min(static_cast<uint32_t>(kArriveGroup), gridDim.x - group * kArriveGroup);
+    *last = counted_last(p.arrived + (1 + group) * kArriveStride, size) && counted_last(p.arrived, groups);
+  }
+  __syncthreads();
+  if (!*last) return;
+  constexpr int WAVES = 4;                      // of 4 or more
+  __shared__ double red[WAVES][3];
+  if (threadIdx.x < WAVES * kWave) {
+    double t[3] = {0.0, 0.0, 0.0};
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += WAVES * kWave)
+      for (int k = 0; k < 3; ++k)
+        t[k] += __builtin_bit_cast(double, __hip_atomic_load(p.part + static_cast<int64_t>(i) * 3 + k, __ATOMIC_RELAXED,
+                                                             __HIP_MEMORY_SCOPE_AGENT));
+    for (int k = 0; k < 3; ++k) {
+      t[k] = wave_sum(t[k]);
+      if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave][k] = t[k];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t[3];
+    for (int k = 0; k < 3; ++k) t[k] = (red[0][k] + red[1][k]) + (red[2][k] + red[3][k]);
+    p.stats[0] = static_cast<float>(p.kl != 0.f ? t[0] + static_cast<double>(p.kl) * t[1] : t[0]);
+    p.stats[1] = static_cast<float>(t[0]);
+    p.stats[2] = static_cast<float>(t[1]);
+    p.stats[3] = static_cast<float>(t[2]);
+  }
+}
+
 template <typename T, int TEAM, int NV, bool LONG, bool NT>
 __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs a, PolArgs p) {
   constexpr int VE = Elem<T>::VE;
@@ -178,10 +239,12 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
   constexpr int CH = NV < 4 ? NV : 4;
   __shared__ Softmax red[2 * NW];
   __shared__ double sums[TEAMS][3];
+  __shared__ int last;
   const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM), tid = threadIdx.x % TEAM;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
   const int nfull = a.vocab / VE, ntail = a.vocab % VE;
-  const float c = a.c;
+  const float c = a.c, clo = a.clo;
+  constexpr bool FINE = kFine<T>;
 
   u32x4 v[NV];
   float tail = -INFINITY;
@@ -214,21 +277,22 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
     if (cur.label >= 0) {
       Softmax t{-INFINITY, 0.0};
 #pragma unroll
-      for (int j = 0; j < NV; j += CH) absorb<T, CH>(t, v + j, c);
-      if (ntail) absorb_one(t, tail, c);
+      for (int j = 0; j < NV; j += CH) absorb<T, CH, FINE>(t, v + j, c, clo);
+      if (ntail) absorb_one<FINE>(t, tail, c, clo);
       if constexpr (LONG) {
-        for (int j0 = NV; j0 * TEAM < nfull; j0 += CH) {
-          u32x4 u[CH];
+        constexpr int CL = 4;
+        for (int j0 = NV; j0 * TEAM < nfull; j0 += CL) {
+          u32x4 u[CL];
 #pragma unroll
-          for (int j = 0; j < CH; ++j) {
+          for (int j = 0; j < CL; ++j) {
             const int idx = (j0 + j) * TEAM + tid;
             u[j] = u32x4{Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf};
             if (idx < nfull) u[j] = load16<NT>(xr + static_cast<int64_t>(idx) * 16);
           }
-          absorb<T, CH>(t, u, c);
+          absorb<T, CL, FINE>(t, u, c, clo);
         }
       }
-      r = team_softmax<TEAM>(t, c, red, parity);
+      r = team_softmax<TEAM, FINE>(t, c, red, parity, clo);
       parity ^= 1;
       logp = log_prob(cur.xl, r, a.scale);
       if (cur.w != 0.f) {
@@ -261,7 +325,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
       const int idx = j * TEAM + tid;
       if (idx < nfull) {
         const int64_t at = static_cast<int64_t>(idx) * 16;
-        store16<NT>(gr + at, zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(v[j], r.m, c, neg));
+        store16<NT>(gr + at, zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(v[j], r.m, c, clo, neg));
         if (fetch) v[j] = load16<NT>(xn + at);
       }
     }
@@ -269,13 +333,13 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
       for (int idx = NV * TEAM + tid; idx < nfull; idx += TEAM) {
         const int64_t at = static_cast<int64_t>(idx) * 16;
         u32x4 o = {0u, 0u, 0u, 0u};
-        if (!zero) o = grad_vec<T>(load16<NT>(xr + at), r.m, c, neg);
+        if (!zero) o = grad_vec<T>(load16<NT>(xr + at), r.m, c, clo, neg);
         store16<NT>(gr + at, o);
       }
     }
     if (tid < ntail) {
       const int64_t e = static_cast<int64_t>(nfull) * VE + tid;
-      Elem<T>::store(gr, e, zero ? 0.f : grad_one<T>(tail, r.m, c, neg));
+      Elem<T>::store(gr, e, zero ? 0.f : grad_one<T>(tail, r.m, c, clo, neg));
       if (fetch) tail = Elem<T>::load(xn, e);
     }
     // the label's entry, over what its owner has just stored there:
@@ -295,32 +359,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
     if (bad) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
   }
   __syncthreads();
-  if (threadIdx.x < 3) {
-    double t = 0.0;
-    for (int i = 0; i < TEAMS; ++i) t += sums[i][threadIdx.x];
-    p.part[static_cast<int64_t>(blockIdx.x) * 3 + threadIdx.x] = t;
-  }
-}
-
-// stats from the workgroups' sums, added in a fixed order.
-__global__ void __launch_bounds__(256) policy_stats_kernel(const double* part, int n, float kl, float* stats) {
-  __shared__ double red[4][3];
-  double t[3] = {0.0, 0.0, 0.0};
-  for (int i = threadIdx.x; i < n; i += 256)
-    for (int q = 0; q < 3; ++q) t[q] += part[i * 3 + q];
-  for (int q = 0; q < 3; ++q) {
-    const double s = wave_sum(t[q]);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x / 64][q] = s;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double s[3];
-    for (int q = 0; q < 3; ++q) s[q] = (red[0][q] + red[1][q]) + (red[2][q] + red[3][q]);
-    stats[0] = static_cast<float>(kl != 0.f ? s[0] + static_cast<double>(kl) * s[1] : s[0]);
-    stats[1] = static_cast<float>(s[0]);
-    stats[2] = static_cast<float>(s[1]);
-    stats[3] = static_cast<float>(s[2]);
-  }
+  policy_stats<TEAMS>(p, sums, &last);
 }
 
 // ---------------------------------------------------------------------------
@@ -403,39 +442,60 @@ struct PrefArgs {
   float beta, eps, w0;
 };
 
-constexpr int kPairThreads = 256;
-
-__device__ inline double block_sum(double v, double* red) {
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x / 64] = v;
-  __syncthreads();
-  return (red[0] + red[1]) + (red[2] + red[3]);
-}
+constexpr int kPairThreads = 1024;
 
 __device__ inline double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
 
 __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a, PrefArgs p) {
-  __shared__ double red[4];
-  const int i = blockIdx.x;
-  double R[2], share[2];
+  constexpr int WAVES = kPairThreads / kWave;
+  __shared__ double red[WAVES][4];
+  const int i = blockIdx.x, tid = threadIdx.x;
   int lo[2], hi[2];
   for (int k = 0; k < 2; ++k) {
     lo[k] = p.offsets[k * p.pairs + i];
     hi[k] = p.offsets[k * p.pairs + i + 1];
+  }
+  for (int k = 0; k < 2; ++k)
     if (lo[k] < 0 || hi[k] < lo[k] || hi[k] > a.rows) {
-      if (threadIdx.x == 0) raise_flag(a.flags, KFAC_FLAG_BAD_INDEX);
+      if (tid == 0) raise_flag(a.flags, KFAC_FLAG_BAD_INDEX);
       lo[k] = hi[k] = 0;
     }
-    double s = 0.0, n = 0.0;
-    for (int64_t r = lo[k] + static_cast<int64_t>(threadIdx.x); r < hi[k]; r += kPairThreads) {
-      const int64_t l = load_index(a.labels, r, a.label_type);
-      if (l < 0 || l >= a.vocab) continue;
-      s += p.wide[r] - (p.ref ? static_cast<double>(p.ref[r]) : 0.0);
-      n += 1.0;
+  // sums of the log ratios and numbers of labelled rows
+  double sum[4] = {0.0, 0.0, 0.0, 0.0};
+  auto take = [&](int k, int64_t label, double wide, float ref) {
+    if (label < 0 || label >= a.vocab) return;
+    sum[2 * k] += wide - static_cast<double>(ref);
+    sum[2 * k + 1] += 1.0;
+  };
+  if (a.rows > 0) {
+    // both sequences' first rows are asked for at once (row 0 for a thread that has none)
+    int64_t label[2];
+    double wide[2];
+    float ref[2];
+    for (int k = 0; k < 2; ++k) {
+      const int64_t r = tid < hi[k] - lo[k] ? lo[k] + tid : 0;
+      label[k] = load_index(a.labels, r, a.label_type);
+      wide[k] = p.wide[r];
+      ref[k] = p.ref ? p.ref[r] : 0.f;
     }
-    s = block_sum(s, red);
-    n = block_sum(n, red);
+    for (int k = 0; k < 2; ++k)
+      if (tid < hi[k] - lo[k]) take(k, label[k], wide[k], ref[k]);
+    for (int k = 0; k < 2; ++k)
+      for (int64_t r = static_cast<int64_t>(lo[k]) + kPairThreads + tid; r < hi[k]; r += kPairThreads)
+        take(k, load_index(a.labels, r, a.label_type), p.wide[r], p.ref ? p.ref[r] : 0.f);
+  }
+  for (int q = 0; q < 4; ++q) {
+    sum[q] = wave_sum(sum[q]);
+    if ((tid & (kWave - 1)) == 0) red[tid / kWave][q] = sum[q];
+  }
+  __syncthreads();
+  double R[2], share[2];
+  for (int k = 0; k < 2; ++k) {
+    double s = 0.0, n = 0.0;
+    for (int w = 0; w < WAVES; ++w) {
+      s += red[w][2 * k];
+      n += red[w][2 * k + 1];
+    }
     share[k] = p.average ? (n > 0.0 ? 1.0 / n : 0.0) : 1.0;
     R[k] = s * share[k];
   }
@@ -497,7 +557,7 @@ __device__ inline void grad_row(const TokArgs& a, const char* x, char* g, int ti
       const int idx = (j0 + j) * TEAM + tid;
       if (idx < nfull)
         store16<NTS>(g + static_cast<int64_t>(idx) * 16,
-                     zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(u[j], m, a.c, neg));
+                     zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(u[j], m, a.c, a.clo, neg));
     }
   }
 }
@@ -534,7 +594,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) preference_grad_kerne
     else grad_row<T, TEAM, UN, false, NT>(a, x, g, tid, ms.x, neg, zero);
     if (tid < ntail) {
       const int64_t e = static_cast<int64_t>(nfull) * VE + tid;
-      Elem<T>::store(g, e, zero ? 0.f : grad_one<T>(Elem<T>::load(x, e), ms.x, a.c, neg));
+      Elem<T>::store(g, e, zero ? 0.f : grad_one<T>(Elem<T>::load(x, e), ms.x, a.c, a.clo, neg));
     }
     if (!zero) {
       const int lv = label / VE;
@@ -577,7 +637,7 @@ int grid_of(int64_t rows, int teams, int per_cu) {
 }
 
 template <typename T, int TEAM, int NV, bool LONG>
-int run_policy(const TokArgs& a, const PolArgs& p, int per_cu, hipStream_t st) {
+void run_policy(const TokArgs& a, const PolArgs& p, int per_cu, hipStream_t st) {
   constexpr int THREADS = TEAM < 256 ? 256 : TEAM;
   const int grid = grid_of(a.rows, THREADS / TEAM, per_cu);
   // the part of a LONG row that is read again is best left in the cache
@@ -585,26 +645,37 @@ int run_policy(const TokArgs& a, const PolArgs& p, int per_cu, hipStream_t st) {
     hipLaunchKernelGGL((policy_kernel<T, TEAM, NV, LONG, !LONG>), dim3(grid), dim3(THREADS), 0, st, a, p);
   else
     hipLaunchKernelGGL((policy_kernel<T, TEAM, NV, LONG, false>), dim3(grid), dim3(THREADS), 0, st, a, p);
-  return grid;
 }
 
-// The team and its registers by the row's length alone.
+// The team and its registers by the row's length alone: the smallest that hold
+// the row, a wavefront a row as far as 512 vectors (no barriers; 16384 x 500
+// bf16 with registers for 256 vectors instead of 64: 21.6 us against 17.3 us).
+// From 4096 vectors one row a workgroup and compute unit: two of half the size
+// would count 512 workgroups' sums in and load no faster (2047 x 50001 bf16 97
+// us, 103 with two).  Past 16384 vectors half of the registers hold the row's
+// start and the other half its stream: with more for the start they spill
+// (1024 x 131072 f32 272 us with 12 vectors, 262 with 8).
 template <typename T>
-int pick_policy(const TokArgs& a, const PolArgs& p, hipStream_t st) {
+void pick_policy(const TokArgs& a, const PolArgs& p, hipStream_t st) {
   const int nvec = a.vocab / Elem<T>::VE;
+  if (nvec <= 64) return run_policy<T, 64, 1, false>(a, p, 6, st);
+  if (nvec <= 64 * 2) return run_policy<T, 64, 2, false>(a, p, 6, st);
   if (nvec <= 64 * 4) return run_policy<T, 64, 4, false>(a, p, 6, st);
+  if (nvec <= 64 * 8) return run_policy<T, 64, 8, false>(a, p, 4, st);
   if (nvec <= 256 * 4) return run_policy<T, 256, 4, false>(a, p, 6, st);
   if (nvec <= 256 * 8) return run_policy<T, 256, 8, false>(a, p, 5, st);
-  if (nvec <= 256 * 16) return run_policy<T, 256, 16, false>(a, p, 4, st);
+  if (nvec <= 512 * 8) return run_policy<T, 512, 8, false>(a, p, 2, st);
   if (nvec <= 1024 * 8) return run_policy<T, 1024, 8, false>(a, p, 1, st);
   if (nvec <= 1024 * 16) return run_policy<T, 1024, 16, false>(a, p, 1, st);
-  return run_policy<T, 1024, 16, true>(a, p, 1, st);
+  return run_policy<T, 1024, 8, true>(a, p, 1, st);
 }
 
 template <typename T>
 void run_logp(const TokArgs& a, const RowStats& rs, hipStream_t st) {
   const int nvec = a.vocab / Elem<T>::VE;
-  if (nvec <= 64 * 8)
+  if (nvec <= 64)
+    hipLaunchKernelGGL((logp_kernel<T, 64, 1>), dim3(grid_of(a.rows, 4, 8)), dim3(256), 0, st, a, rs);
+  else if (nvec <= 64 * 8)
     hipLaunchKernelGGL((logp_kernel<T, 64, 4>), dim3(grid_of(a.rows, 4, 8)), dim3(256), 0, st, a, rs);
   else if (a.rows >= 2 * kCus)
     hipLaunchKernelGGL((logp_kernel<T, 256, 8>), dim3(grid_of(a.rows, 1, 8)), dim3(256), 0, st, a, rs);
@@ -618,9 +689,12 @@ void run_pref_grad(const TokArgs& a, const PrefArgs& p, const RowStats& rs, hipS
   if (nvec <= 64 * 8)
     hipLaunchKernelGGL((preference_grad_kernel<T, 64, 4, NT>), dim3(1 + grid_of(a.rows, 4, 8)), dim3(256), 0, st, a,
                        p, rs);
-  else
+  else if (NT || a.rows >= 2 * kCus)
     hipLaunchKernelGGL((preference_grad_kernel<T, 256, 4, NT>), dim3(1 + grid_of(a.rows, 1, 8)), dim3(256), 0, st, a,
                        p, rs);
+  else      // few rows: 1024 threads each (160 rows of 16384 f32: 11 us with 256)
+    hipLaunchKernelGGL((preference_grad_kernel<T, 1024, 4, false>), dim3(1 + grid_of(a.rows, 1, 2)), dim3(1024), 0, st,
+                       a, p, rs);
 }
 
 template <typename T>
@@ -640,9 +714,12 @@ kfac_status_t run_preference(const TokArgs& a, const PrefArgs& q, RowStats rs, h
   return KFAC_OK;
 }
 
-// Workspace behind the flag word.  policy: part [kMaxPartials][3] double.
-// preference: part [pairs][4] double, stat [rows] float2, wide [rows] double,
+// Workspace behind the flag word.  policy: part [kMaxPartials][3] double, the
+// counters.  preference: part [pairs][4] double, stat [rows] float2, wide [rows] double,
 // coef [rows] float.
+constexpr size_t kPolicyParts = kFlagBytes + sizeof(double) * 3 * kMaxPartials;
+constexpr size_t kArriveBytes = sizeof(uint32_t) * kArriveStride * (1 + kMaxPartials / kArriveGroup);
+static_assert(kPolicyParts % 256 == 0 && kArriveBytes % 256 == 0 && kMaxPartials % kArriveGroup == 0);
 struct PrefRegions {
   size_t part, stat, wide, coef, end;
 };
@@ -659,7 +736,7 @@ PrefRegions pref_regions(int64_t rows, int32_t pairs) {
 }  // namespace
 
 size_t token_workspace_bytes(int objective, int64_t rows, int32_t groups) {
-  if (objective == KFAC_OBJ_POLICY) return kFlagBytes + align_up(sizeof(double) * 3 * kMaxPartials, 256);
+  if (objective == KFAC_OBJ_POLICY) return kPolicyParts + kArriveBytes;
   if (objective == KFAC_OBJ_PREFERENCE) return pref_regions(rows, groups).end;
   return kFlagBytes;
 }
@@ -687,14 +764,15 @@ kfac_status_t launch_policy(const kfac_token_rows_t& t, const kfac_policy_t& p, 
   q.weight = p.weight;
   q.old_logp = p.old_logp;
   q.ref = p.ref_logp;
-  q.part = reinterpret_cast<double*>(ws + kFlagBytes);
+  q.part = reinterpret_cast<uint64_t*>(ws + kFlagBytes);
   q.lo = static_cast<float>(1.0 - static_cast<double>(p.clip_low));
   q.hi = static_cast<float>(1.0 + static_cast<double>(p.clip_high));
   q.kl = p.kl_coef;
+  q.stats = p.stats;
+  q.arrived = reinterpret_cast<uint32_t*>(ws + kPolicyParts);
   q.w0 = static_cast<float>(1.0 / static_cast<double>(t.rows));
-  const int n = t.dtype == KFAC_BF16 ? pick_policy<__bf16>(a, q, st) : pick_policy<float>(a, q, st);
-  KFAC_HIP_TRY(hipGetLastError());
-  hipLaunchKernelGGL(policy_stats_kernel, dim3(1), dim3(256), 0, st, q.part, n, p.kl_coef, p.stats);
+  if (t.dtype == KFAC_BF16) pick_policy<__bf16>(a, q, st);
+  else pick_policy<float>(a, q, st);
   KFAC_HIP_TRY(hipGetLastError());
   return KFAC_OK;
 }
