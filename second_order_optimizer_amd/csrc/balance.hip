@@ -20,13 +20,12 @@
 // has out of the sums; both compute the same gradient there.  E below a vector:
 // one element a lane.
 //
-// 65536 tokens of 256 bf16 logits: first pass 13.8 us (arithmetic, some 14
-// operations an element with the exponential counting four, and the memory's
-// latency at either end: four tokens a lane in all), sums 4.6 us (latency),
-// second pass 16.5 us (67 MB through the cache at 4.1 TB/s).  The next token's
-// logits are loaded while one is worked on, and 8 wavefronts fit a SIMD.  With
-// workgroups of 512, the mask waited for before the logits and the softmax
-// found twice it was 15.5, 4.6 and 22 us.
+// Bound by memory and its latency at these sizes, not by arithmetic.  65536
+// tokens of 256 bf16 logits: first pass 13.9 us (34 MB in; 12.8 without its
+// exponentials), sums 4.6 us (latency), second pass 16.5 us (67 MB through the
+// cache).  The next token's logits are loaded while one is worked on, and 8
+// wavefronts fit a SIMD.  With workgroups of 512, the mask waited for before
+// the logits and the softmax found twice it was 15.5, 4.6 and 22 us.
 #include "objectives.h"
 
 #include <algorithm>

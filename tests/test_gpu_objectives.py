@@ -106,6 +106,17 @@ def test_logp_many_rows(Q, rows):
         near(got, O.token_logp(xd, labels), logp_tolerance(xd, labels, 1.0))
 
 
+@pytest.mark.parametrize("rows,vocab,dtype", [(20011, 40, "bf16"), (20011, 700, "f32"), (600001, 9, "bf16"),
+                                              (530000, 5, "f32")])
+def test_logp_rows_beyond_the_teams(Q, rows, vocab, dtype):
+    """Each team walks several rows; short ones are finished up to 64 at a time, and 8192 teams of them are resident."""
+    rng = np.random.default_rng(rows)
+    x, xd = matrix(rng, rows, vocab, dtype)
+    labels = rng.integers(-1, vocab, rows).astype(np.int32)
+    got = Q.TokenLogp(rows, vocab, dtype).run(x, gpu(labels))
+    near(got, O.token_logp(xd, labels), np.where(labels >= 0, logp_tolerance(xd, labels, 1.0), 0))
+
+
 def policy_inputs(rng, xd, labels, s):
     logp = O.token_logp(xd, labels, s)
     n = labels.size
