@@ -20,12 +20,16 @@
 // has out of the sums; both compute the same gradient there.  E below a vector:
 // one element a lane.
 //
-// Bound by memory and its latency at these sizes, not by arithmetic.  65536
-// tokens of 256 bf16 logits: first pass 13.9 us (34 MB in; 12.8 without its
-// exponentials), sums 4.6 us (latency), second pass 16.5 us (67 MB through the
-// cache).  The next token's logits are loaded while one is worked on, and 8
-// wavefronts fit a SIMD.  With workgroups of 512, the mask waited for before
-// the logits and the softmax found twice it was 15.5, 4.6 and 22 us.
+// 65536 tokens of 256 bf16 logits: first pass 14.1 us, sums 4.5 us (latency),
+// second pass 11.8 us, where a copy of the same 34 MB takes 10.3 us.  The first
+// pass issues some 115 vector operations for a lane's eight logits (6.7 us in
+// all; only 1 us of it the exponentials' own rate), the rest is the launch, the
+// first loads and the sums at the end.  The next token's logits are loaded while
+// one is worked on, tokens are numbered in 32 bits with rows stepped to, and 8
+// wavefronts fit a SIMD.  With workgroups of 512, the mask waited for before the
+// logits, addresses multiplied out, every lane dividing for the scales and the
+// softmax found twice it was 15.5, 4.6 and 22 us; two vectors a lane and half
+// the lanes: 17.1, 4.8 and 11.3 us.
 #include "objectives.h"
 
 #include <algorithm>
@@ -36,7 +40,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kGradThreads = 256, kGradBlocks = 2048;
-constexpr int kSmallRounds = 8;
+constexpr int kSmallRounds = 4;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct BalArgs {
@@ -61,6 +65,7 @@ struct BalArgs {
   float* f;              // [E]: a count's weight in the gradient
   float2* stat;          // [tokens]: (maximum, 1 / sum), the latter 0 for a token that does not count
   double* total;         // [2]: n, sum of lse^2
+  float* zs;             // [1]: lse's weight in the gradient
 };
 
 // Sum (maximum) over the LPT lanes of a token; every lane gets it.
@@ -126,9 +131,8 @@ struct Columns {
 
 // A lane's part of a token's logits, minus infinity past the row.
 template <typename S>
-__device__ inline void load_row(u32x4 (&v)[S::NV], const BalArgs& a, int64_t t, const Columns<S>& cols) {
+__device__ inline void load_row(u32x4 (&v)[S::NV], const char* row, const Columns<S>& cols) {
   using T = typename S::T;
-  const char* row = a.x + t * a.ldx;
 #pragma unroll
   for (int q = 0; q < S::NV; ++q) {
     v[q] = u32x4{Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf};
@@ -148,12 +152,12 @@ struct TokenIn {
   u32x4 v[S::NV];
   uint8_t live;
 
-  __device__ void load(const BalArgs& a, int64_t t, const Columns<S>& cols) {
+  __device__ void load(const BalArgs& a, uint32_t t, const char* row, const Columns<S>& cols) {
 #pragma unroll
     for (int q = 0; q < S::NV; ++q) v[q] = u32x4{0u, 0u, 0u, 0u};
     live = 0;
-    if (t >= a.tokens) return;
-    load_row<S>(v, a, t, cols);
+    if (t >= static_cast<uint32_t>(a.tokens)) return;
+    load_row<S>(v, row, cols);
     live = a.mask ? a.mask[t] : 1;
   }
   // The logits, minus infinity past the row; zeros for a token that does not count.
@@ -184,19 +188,30 @@ __device__ inline float row_maximum(const float (&x)[S::NV][S::VEC]) {
   return group_reduce<S::LPT, true>(m);
 }
 
-// First pass over a wavefront's tokens t0 + slot, t0 + stride + slot, ..., the
-// first of which is loaded: adds p to the lane's columns, lse^2 and the tokens
+// A lane's tokens in either pass: every `stride`th from t, with its row in a
+// matrix of `ld` bytes a row.  Tokens are numbered in 32 bits, with room for one
+// stride past the last.
+struct Tokens {
+  uint32_t t, stride;
+  int64_t step;
+  __device__ Tokens(int64_t first, int64_t every, int64_t ld)
+      : t(static_cast<uint32_t>(first)), stride(static_cast<uint32_t>(every)), step(every * ld) {}
+};
+
+// First pass over a lane's tokens, the first of which is loaded: adds p to the lane's columns, lse^2 and the tokens
 // that count (in a token's first lane); keeps each token's maximum and 1 / sum.
 template <typename S>
-__device__ inline void count_tokens(const BalArgs& a, const Columns<S>& cols, int64_t t0, int64_t stride,
+__device__ inline void count_tokens(const BalArgs& a, const Columns<S>& cols, Tokens at, const char* row,
                                     TokenIn<S> in, float (&acc)[S::NV][S::VEC], double& z, int& n) {
   const int lane = threadIdx.x & (kWave - 1), slot = lane / S::LPT, sub = lane % S::LPT;
-  for (; t0 < a.tokens; t0 += stride) {
-    const int64_t t = t0 + slot;
+  const uint32_t tokens = static_cast<uint32_t>(a.tokens);
+  for (; at.t - slot < tokens; at.t += at.stride) {       // as long as the wavefront's first token is one
+    const uint32_t t = at.t;
     float x[S::NV][S::VEC];
     const bool live = in.live != 0;
     in.expand(x);
-    in.load(a, t + stride, cols);
+    row += at.step;
+    in.load(a, t + at.stride, row, cols);
     if constexpr (!S::EVEN) {
 #pragma unroll
       for (int q = 0; q < S::NV; ++q)
@@ -214,7 +229,7 @@ __device__ inline void count_tokens(const BalArgs& a, const Columns<S>& cols, in
       }
     s = group_reduce<S::LPT, false>(s);
     const float inv = live ? inverse(s) : 0.f;
-    if (sub == 0 && t < a.tokens) a.stat[t] = make_float2(m, inv);
+    if (sub == 0 && t < tokens) a.stat[t] = make_float2(m, inv);
 #pragma unroll
     for (int q = 0; q < S::NV; ++q)
 #pragma unroll
@@ -283,34 +298,59 @@ __device__ inline void column_sums(const Columns<S>& cols, const float (&acc)[S:
     }
 }
 
+// The lane's columns of an array [E].
+template <typename S>
+__device__ inline void own_columns(float (&f)[S::NV][S::VEC], const float* from, const Columns<S>& cols) {
+#pragma unroll
+  for (int q = 0; q < S::NV; ++q) {
+#pragma unroll
+    for (int i = 0; i < S::VEC; ++i) f[q][i] = 0.f;
+    if (cols.skip[q] < S::VEC) {
+      if constexpr (S::VEC == 1) {
+        f[q][0] = from[cols.col[q]];
+      } else {
+#pragma unroll
+        for (int k = 0; k < S::VEC / 4; ++k) {
+          const u32x4 v = load16(from + cols.col[q] + 4 * k);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[q][4 * k + i] = __uint_as_float(v[i]);
+        }
+      }
+    }
+  }
+}
+
 // Second pass: the gradients, from each token's maximum and inverse sum as the
-// first pass found them (a third less arithmetic than to find them again:
-// 65536 x 256 bf16 22 -> 16.5 us with the loads ahead), from f of the lane's
-// columns and zs = 2 z_coef / n (both times grad_scale).
+// first pass found them (a third less arithmetic than to find them again), from
+// f of the lane's columns and zs = 2 z_coef / n (both times grad_scale).
 template <typename S>
 struct TokenBack {
   u32x4 v[S::NV];
   float2 stat;
 
-  __device__ void load(const BalArgs& a, int64_t t, const Columns<S>& cols) {
+  __device__ void load(const BalArgs& a, uint32_t t, const char* row, const Columns<S>& cols) {
 #pragma unroll
     for (int q = 0; q < S::NV; ++q) v[q] = u32x4{0u, 0u, 0u, 0u};
     stat = make_float2(0.f, 0.f);
-    if (t >= a.tokens) return;
-    load_row<S>(v, a, t, cols);
+    if (t >= static_cast<uint32_t>(a.tokens)) return;
+    load_row<S>(v, row, cols);
     stat = a.stat[t];
   }
 };
 
 template <typename S>
-__device__ inline void grad_tokens(const BalArgs& a, const Columns<S>& cols, int64_t t0, int64_t stride,
+__device__ inline void grad_tokens(const BalArgs& a, const Columns<S>& cols, Tokens at, const char* row,
                                    TokenBack<S> in, const float (&f)[S::NV][S::VEC], float zs) {
   using T = typename S::T;
   const int slot = (threadIdx.x & (kWave - 1)) / S::LPT;
-  for (; t0 < a.tokens; t0 += stride) {
-    const int64_t t = t0 + slot;
+  const uint32_t tokens = static_cast<uint32_t>(a.tokens);
+  const int64_t grad_step = static_cast<int64_t>(at.stride) * a.ldg;
+  char* grad = a.g + static_cast<int64_t>(at.t) * a.ldg;
+  for (; at.t - slot < tokens; at.t += at.stride, grad += grad_step) {
+    const uint32_t t = at.t;
     const TokenBack<S> cur = in;
-    in.load(a, t + stride, cols);
+    row += at.step;
+    in.load(a, t + at.stride, row, cols);
     const float m = cur.stat.x, inv = cur.stat.y;
     float p[S::NV][S::VEC], pf = 0.f;
 #pragma unroll
@@ -323,16 +363,15 @@ __device__ inline void grad_tokens(const BalArgs& a, const Columns<S>& cols, int
     pf = group_reduce<S::LPT, false>(pf);
     const bool live = inv != 0.f;
     const float shift = (zs != 0.f ? zs * fmaf(__builtin_amdgcn_logf(inv), -kLn2, m) : 0.f) - pf;
-    if (t >= a.tokens) continue;
-    char* row = a.g + t * a.ldg;
+    if (t >= tokens) continue;
 #pragma unroll
     for (int q = 0; q < S::NV; ++q) {
       if (cols.skip[q] < S::VEC) {
         float g[S::VEC];
 #pragma unroll
         for (int i = 0; i < S::VEC; ++i) g[i] = p[q][i] * (f[q][i] + shift);
-        if constexpr (S::VEC == 1) Elem<T>::store(row, cols.col[q], live ? g[0] : 0.f);
-        else store16(row + static_cast<int64_t>(cols.col[q]) * sizeof(T), live ? pack16<T>(g) : u32x4{0u, 0u, 0u, 0u});
+        if constexpr (S::VEC == 1) Elem<T>::store(grad, cols.col[q], live ? g[0] : 0.f);
+        else store16(grad + static_cast<int64_t>(cols.col[q]) * sizeof(T), live ? pack16<T>(g) : u32x4{0u, 0u, 0u, 0u});
       }
     }
   }
@@ -372,8 +411,10 @@ struct CountShared {
     const int64_t per = static_cast<int64_t>(WAVES) * S::SLOTS, t0 = block * per + wid * S::SLOTS, stride = blocks * per;
     const int64_t first = static_cast<int64_t>(block) * kThreads + threadIdx.x;
     const int64_t threads = static_cast<int64_t>(blocks) * kThreads;
+    const Tokens at(t0 + (threadIdx.x & (kWave - 1)) / S::LPT, stride, a.ldx);
+    const char* row = a.x + static_cast<int64_t>(at.t) * a.ldx;
     TokenIn<S> in;
-    in.load(a, t0 + (threadIdx.x & (kWave - 1)) / S::LPT, cols);
+    in.load(a, at.t, row, cols);
     Chosen chosen;
     chosen.load(a, first, threads);
     for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
@@ -381,7 +422,7 @@ struct CountShared {
     float acc[S::NV][S::VEC] = {};
     double zs = 0.0;
     int ns = 0;
-    count_tokens<S>(a, cols, t0, stride, in, acc, zs, ns);
+    count_tokens<S>(a, cols, at, row, in, acc, zs, ns);
     chosen.count(a, hist, first, threads);
     column_sums<S>(cols, acc, psum[wid]);
     zs = wave_sum(zs);
@@ -477,6 +518,7 @@ __global__ void __launch_bounds__(1024) balance_reduce_kernel(BalArgs a) {
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       a.total[0] = n;
       a.total[1] = z;
+      *a.zs = Scales(a, n).zs(a);
     }
   }
 }
@@ -486,23 +528,21 @@ __global__ void __launch_bounds__(kGradThreads, S::WAVES) balance_grad_kernel(Ba
   const int lane = threadIdx.x & (kWave - 1), wid = threadIdx.x / kWave;
   const Columns<S> cols(lane % S::LPT, a.E);
   const int64_t per = static_cast<int64_t>(kGradThreads / kWave) * S::SLOTS;
-  const int64_t t0 = blockIdx.x * per + wid * S::SLOTS, stride = gridDim.x * per;
+  const Tokens at(blockIdx.x * per + wid * S::SLOTS + lane / S::LPT, gridDim.x * per, a.ldx);
+  const char* row = a.x + static_cast<int64_t>(at.t) * a.ldx;
   TokenBack<S> in;
-  in.load(a, t0 + lane / S::LPT, cols);
+  in.load(a, at.t, row, cols);
   float f[S::NV][S::VEC];
-#pragma unroll
-  for (int q = 0; q < S::NV; ++q)
-#pragma unroll
-    for (int i = 0; i < S::VEC; ++i) f[q][i] = cols.skip[q] < S::VEC ? a.f[cols.col[q] + i] : 0.f;
-  const double live = a.total[0];
-  const Scales sc(a, live);
+  own_columns<S>(f, a.f, cols);
+  const float zs = *a.zs;
   if (blockIdx.x == 0 && wid == 0) {
+    const double live = a.total[0];
     double dot = 0.0;
     for (int e = lane; e < a.E; e += kWave) dot += a.counts[e] * a.prob64[e];
     dot = wave_sum(dot);
-    if (lane == 0) sc.write(a, dot, a.total[1], live);
+    if (lane == 0) Scales(a, live).write(a, dot, a.total[1], live);
   }
-  grad_tokens<S>(a, cols, t0, stride, in, f, sc.zs(a));
+  grad_tokens<S>(a, cols, at, row, in, f, zs);
 }
 
 // All of it in one workgroup, for a few tokens.
@@ -539,9 +579,11 @@ __global__ void __launch_bounds__(kThreads) balance_small_kernel(BalArgs a) {
     for (int i = 0; i < S::VEC; ++i)
       f[q][i] = cols.skip[q] < S::VEC ? static_cast<float>(unit * sh.hist[cols.col[q] + i]) : 0.f;
   const int64_t per = static_cast<int64_t>(Shared::WAVES) * S::SLOTS;
+  const Tokens at(wid * S::SLOTS + lane / S::LPT, per, a.ldx);
+  const char* row = a.x + static_cast<int64_t>(at.t) * a.ldx;
   TokenBack<S> in;
-  in.load(a, wid * S::SLOTS + lane / S::LPT, cols);
-  grad_tokens<S>(a, cols, wid * S::SLOTS, per, in, f, sc.zs(a));
+  in.load(a, at.t, row, cols);
+  grad_tokens<S>(a, cols, at, row, in, f, sc.zs(a));
 }
 
 template <typename S>
@@ -639,6 +681,7 @@ kfac_status_t launch_balance(const kfac_balance_t& b, char* ws, hipStream_t st) 
   a.f = reinterpret_cast<float*>(ws + r.f);
   a.stat = reinterpret_cast<float2*>(ws + r.stat);
   a.total = reinterpret_cast<double*>(ws + r.total);
+  a.zs = reinterpret_cast<float*>(a.total + 2);
   return b.dtype == KFAC_BF16 ? pick<__bf16>(a, st) : pick<float>(a, st);
 }
 
