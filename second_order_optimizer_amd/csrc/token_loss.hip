@@ -472,11 +472,11 @@ struct PrefArgs {
 
 constexpr int kPairThreads = 1024;
 
-__device__ inline double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
-
 __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a, PrefArgs p) {
   constexpr int WAVES = kPairThreads / kWave;
+  static_assert(WAVES == 16, "row_sum adds 16 lanes");
   __shared__ double red[WAVES][4];
+  __shared__ float coef[2];
   const int i = blockIdx.x, tid = threadIdx.x;
   int lo[2], hi[2];
   for (int k = 0; k < 2; ++k) {
@@ -488,15 +488,16 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a
       if (tid == 0) raise_flag(a.flags, KFAC_FLAG_BAD_INDEX);
       lo[k] = hi[k] = 0;
     }
-  // sums of the log ratios and numbers of labelled rows
+  // sums of the log ratios and, where they are averaged, numbers of labelled rows
   double sum[4] = {0.0, 0.0, 0.0, 0.0};
-  auto take = [&](int k, int64_t label, double wide, float ref) {
-    if (label < 0 || label >= a.vocab) return;
+  auto labelled = [&](int64_t label) { return label >= 0 && label < a.vocab; };
+  auto take = [&](int k, double wide, float ref) {
     sum[2 * k] += wide - static_cast<double>(ref);
     sum[2 * k + 1] += 1.0;
   };
+  bool first[2] = {false, false};       // the thread's first row of either sequence has a label
   if (a.rows > 0) {
-    // both sequences' first rows are asked for at once (row 0 for a thread that has none)
+    // both are asked for at once (row 0 for a thread that has none)
     int64_t label[2];
     double wide[2];
     float ref[2];
@@ -506,59 +507,66 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a
       wide[k] = p.wide[r];
       ref[k] = p.ref ? p.ref[r] : 0.f;
     }
-    for (int k = 0; k < 2; ++k)
-      if (tid < hi[k] - lo[k]) take(k, label[k], wide[k], ref[k]);
+    for (int k = 0; k < 2; ++k) {
+      first[k] = tid < hi[k] - lo[k] && labelled(label[k]);
+      if (first[k]) take(k, wide[k], ref[k]);
+    }
     for (int k = 0; k < 2; ++k)
       for (int64_t r = static_cast<int64_t>(lo[k]) + kPairThreads + tid; r < hi[k]; r += kPairThreads)
-        take(k, load_index(a.labels, r, a.label_type), p.wide[r], p.ref ? p.ref[r] : 0.f);
+        if (labelled(load_index(a.labels, r, a.label_type))) take(k, p.wide[r], p.ref ? p.ref[r] : 0.f);
   }
   for (int q = 0; q < 4; ++q) {
+    if ((q & 1) && !p.average) continue;
     sum[q] = wave_sum(sum[q]);
     if ((tid & (kWave - 1)) == 0) red[tid / kWave][q] = sum[q];
   }
   __syncthreads();
-  double R[2], share[2];
-  for (int k = 0; k < 2; ++k) {
-    double s = 0.0, n = 0.0;
-    for (int w = 0; w < WAVES; ++w) {
-      s += red[w][2 * k];
-      n += red[w][2 * k + 1];
+  // one wavefront forms the loss (in all of them its 64-bit functions took 1.6 us more)
+  if (tid < kWave) {
+    double R[2], share[2];
+    for (int k = 0; k < 2; ++k) {
+      const double s = lane_of(row_sum(red[tid % WAVES][2 * k]), 0);
+      const double n = p.average ? lane_of(row_sum(red[tid % WAVES][2 * k + 1]), 0) : 0.0;
+      share[k] = p.average ? (n > 0.0 ? 1.0 / n : 0.0) : 1.0;
+      R[k] = s * share[k];
     }
-    share[k] = p.average ? (n > 0.0 ? 1.0 / n : 0.0) : 1.0;
-    R[k] = s * share[k];
-  }
-  const double h = R[0] - R[1], beta = p.beta, eps = p.eps;
-  const double w = p.weight ? static_cast<double>(p.weight[i]) : static_cast<double>(p.w0);
-  double loss, slope;
-  if (p.kind == KFAC_PREF_SIGMOID) {
-    const double x = beta * h;
-    loss = (1.0 - eps) * softplus(-x);
-    if (eps != 0.0) loss += eps * softplus(x);      // no 0 times infinity where x is infinite
-    // sigma(x) - (1 - e), with sigma of the side that does not cancel
-    const double sig = 1.0 / (1.0 + exp(fabs(x)));    // sigma(-|x|)
-    slope = beta * (x >= 0.0 ? eps - sig : sig - (1.0 - eps));
-  } else {
-    const double x = h - 0.5 / beta;
-    loss = x * x;
-    slope = 2.0 * x;
-  }
-  if (threadIdx.x == 0) {
-    p.seq[i] = static_cast<float>(R[0]);
-    p.seq[p.pairs + i] = static_cast<float>(R[1]);
-    double* q = p.part + static_cast<int64_t>(i) * 4;
-    q[0] = w != 0.0 ? w * loss : 0.0;
-    q[1] = h > 0.0 ? w : 0.0;
-    q[2] = w != 0.0 ? w * beta * h : 0.0;
-    q[3] = w;
-    if (w != 0.0 && !(fabs(loss) < INFINITY)) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
-  }
-  for (int k = 0; k < 2; ++k) {
-    const double f = w != 0.0 ? (k ? -w : w) * slope * share[k] * static_cast<double>(a.grad_scale) : 0.0;
-    if (threadIdx.x == 0 && !(fabsf(static_cast<float>(f)) < INFINITY)) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
-    for (int64_t r = lo[k] + static_cast<int64_t>(threadIdx.x); r < hi[k]; r += kPairThreads) {
-      const int64_t l = load_index(a.labels, r, a.label_type);
-      p.coef[r] = l >= 0 && l < a.vocab ? static_cast<float>(f) : 0.f;
+    const double h = R[0] - R[1], beta = p.beta, eps = p.eps;
+    const double w = p.weight ? static_cast<double>(p.weight[i]) : static_cast<double>(p.w0);
+    double loss, slope;
+    if (p.kind == KFAC_PREF_SIGMOID) {
+      const double x = beta * h, e = exp(-fabs(x)), l = log1p(e);
+      loss = (1.0 - eps) * (fmax(-x, 0.0) + l);                 // log(1 + exp(-x)), and of x below
+      if (eps != 0.0) loss += eps * (fmax(x, 0.0) + l);         // no 0 times infinity where x is infinite
+      // sigma(x) - (1 - e), with sigma of the side that does not cancel
+      const double sig = e / (1.0 + e);                         // sigma(-|x|)
+      slope = beta * (x >= 0.0 ? eps - sig : sig - (1.0 - eps));
+    } else {
+      const double x = h - 0.5 / beta;
+      loss = x * x;
+      slope = 2.0 * x;
     }
+    if (tid == 0) {
+      p.seq[i] = static_cast<float>(R[0]);
+      p.seq[p.pairs + i] = static_cast<float>(R[1]);
+      double* q = p.part + static_cast<int64_t>(i) * 4;
+      q[0] = w != 0.0 ? w * loss : 0.0;
+      q[1] = h > 0.0 ? w : 0.0;
+      q[2] = w != 0.0 ? w * beta * h : 0.0;
+      q[3] = w;
+      bool bad = w != 0.0 && !(fabs(loss) < INFINITY);
+      for (int k = 0; k < 2; ++k) {
+        coef[k] = w != 0.0 ? static_cast<float>((k ? -w : w) * slope * share[k] * static_cast<double>(a.grad_scale)) : 0.f;
+        bad |= !(fabsf(coef[k]) < INFINITY);
+      }
+      if (bad) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
+    }
+  }
+  __syncthreads();
+  for (int k = 0; k < 2; ++k) {
+    const float f = coef[k];
+    if (tid < hi[k] - lo[k]) p.coef[lo[k] + tid] = first[k] ? f : 0.f;
+    for (int64_t r = static_cast<int64_t>(lo[k]) + kPairThreads + tid; r < hi[k]; r += kPairThreads)
+      p.coef[r] = labelled(load_index(a.labels, r, a.label_type)) ? f : 0.f;
   }
 }
 
