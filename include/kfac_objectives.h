@@ -104,7 +104,8 @@ typedef struct kfac_policy {
  *     squared: L = (h - 1 / (2 beta))^2
  *     loss = sum w L
  * A pair of weight 0 counts for nothing.  Rows outside every sequence have
- * gradient 0.
+ * gradient 0.  Where decreasing offsets (flagged) leave rows to two sequences,
+ * they have the gradient of one of them.
  */
 typedef struct kfac_preference {
   const int32_t* offsets;    /* [2 pairs + 1], device, not decreasing, within [0, rows] */
@@ -164,7 +165,8 @@ typedef struct kfac_balance {
  * the block's eight columns, and an element is kept when its draw is at least
  * T.  The same seed, offset and shape give the same mask in any call, so the
  * backward pass is the same call on the output gradient, without residual.
- * A dropped value is 0 whatever x holds there.
+ * A dropped value is 0 whatever x holds there.  At most 2^32 - 1024 blocks
+ * (2^35 elements) a call.
  */
 typedef struct kfac_dropout {
   const void* x;           /* [rows, cols], row stride ld */

@@ -173,9 +173,9 @@ __device__ inline float grad_one(float x, float m, float c, float clo, float neg
 // and stores stay mixed and no phase waits for an empty pipe.  LONG: rows
 // beyond the registers (TEAM * NV vectors) read the rest twice.
 //
-// Bound by HBM with reads and writes mixed: 4096 x 131072 bf16 425 us, 5.1 TB/s
+// Bound by HBM with reads and writes mixed: 4096 x 131072 bf16 424 us, 5.1 TB/s
 // (a copy as large: 6.2); without the exponentials it is 2% less.  2047 x 50001
-// bf16 91 us, 4.5 TB/s: eight rows a compute unit, so the first loads and the
+// bf16 92 us, 4.4 TB/s: eight rows a compute unit, so the first loads and the
 // last stores, with nothing to pair them with, are a ninth each.
 
 struct RowScalars {
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
 // time.  logp is formed in 64 bits, since the preference loss adds up small
 // differences of it; with `stat` each row's (M, 1 / S) and with `wide` its logp
 // in 64 bits are kept for the kernels below.  Rows before `past` are read past
-// the cache.  Bound by HBM reads: 8192 x 32768 bf16 86.6 us, 6.2 TB/s; 1024 x
+// the cache.  Bound by HBM reads: 8192 x 32768 bf16 86 us, 6.2 TB/s; 1024 x
 // 131072 f32 81 us, 6.6 TB/s.  64 rows of 32768: 5 us, of which the launch is
 // half.  Wavefronts a row by the rows there are: 1024 threads where 256 would
 // leave compute units idle.
@@ -611,10 +611,10 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a
 // coefficient.  The rows are taken last to first: where logits and gradients
 // do not fit the cache, the first pass reads all but its last rows past it
 // and the gradients are stored past it, so that those last rows are still
-// there (the whole loss 287 -> 250 us on 7200 rows of 32768 bf16 logits).  The
+// there (the whole loss 287 -> 250 us on 7200 rows of 32768 bf16 logits, 243 now).  The
 // extra workgroup adds up the pairs' statistics.  Bound by memory: 165 us for
-// the 944 MB of these rows and gradients (5.7 TB/s), after 76 us of first pass
-// and 6.5 us between; the second read is the price of a coefficient that needs
+// the 0.94 GB of these rows and gradients (5.7 TB/s), after 78 us of first pass
+// and 5 us between; the second read is the price of a coefficient that needs
 // the whole pair.
 template <typename T, int TEAM, int UN, bool NTL, bool NTS>
 __device__ inline void grad_row(const TokArgs& a, const char* x, char* g, int tid, float m, float neg, bool zero) {
