@@ -172,6 +172,19 @@ def test_policy_more_rows_than_teams(Q, rows, vocab, dtype):
     check_policy(Q, np.random.default_rng(rows), rows, vocab, dtype, 0.02, 1.0, pad=3)
 
 
+@pytest.mark.parametrize("rows,vocab,dtype", [(1, 90, "bf16"), (130, 90, "f32"), (7001, 90, "bf16"), (3100, 1200, "f32")])
+def test_policy_statistics_over_many_workgroups(Q, rows, vocab, dtype):
+    """From one workgroup to all that are resident, counted in groups; the same object again gives the same."""
+    rng = np.random.default_rng(rows + vocab)
+    check_policy(Q, rng, rows, vocab, dtype, 0.02, 1.0)
+    x = torch.randn(rows, vocab, device="cuda").to(DT[dtype])
+    lab, adv = torch.randint(0, vocab, (rows,), device="cuda"), torch.randn(rows, device="cuda")
+    op = Q.PolicyLoss(rows, vocab, dtype)
+    first = op.run(x, lab, adv)
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(first, op.run(x, lab, adv)))
+
+
 @pytest.mark.parametrize("vocab,dtype", [(9, "bf16"), (3001, "bf16"), (70001, "f32"), (140003, "bf16")])
 def test_policy_in_place_and_defaults(Q, vocab, dtype):
     rng = np.random.default_rng(5)
