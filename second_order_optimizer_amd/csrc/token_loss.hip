@@ -13,6 +13,7 @@
 // in float32 and the vectors of a thread, the threads and the wavefronts in
 // 64 bits, in a fixed order; the gradient is rounded once, when it is stored.
 #include "objectives.h"
+#include "objectives_grid.h"
 
 #include <algorithm>
 #include <cfloat>
@@ -21,8 +22,6 @@
 namespace kfac {
 
 namespace {
-
-constexpr int kCus = 256;
 
 struct TokArgs {
   const char* x;
@@ -706,17 +705,6 @@ TokArgs tok_args(const kfac_token_rows_t& t, char* ws) {
   a.grad_scale = t.logit_scale * t.grad_scale;
   a.flags = reinterpret_cast<uint32_t*>(ws);
   return a;
-}
-
-// Workgroups for so many rows: as many as are resident.  Of workgroups with a row
-// each at a time, fewer that all walk as many rows (4096 x 12000 bf16 47.5 ->
-// 44.7 us); with four short rows at a time arithmetic counts and that loses
-// (16384 x 500 17.2 -> 19.3 us).
-int grid_of(int64_t rows, int teams, int per_cu) {
-  const int64_t need = (rows + teams - 1) / teams, most = static_cast<int64_t>(kCus) * per_cu;
-  if (teams > 1) return static_cast<int>(std::min(need, most));
-  const int64_t rounds = (need + most - 1) / most;
-  return static_cast<int>((need + rounds - 1) / rounds);
 }
 
 template <typename T, int TEAM, int NV, bool LONG>
