@@ -13,7 +13,11 @@
  * hipStream_t the calls only enqueue on, `workspace` 256-byte aligned with a
  * sticky flag word at its start (kfac_read_flags reads it), zeroed whole
  * once by the caller, one workspace for one call at a time; arguments are validated
- * before anything is enqueued.  Differences: matrices are row-major with a
+ * before anything is enqueued.  The objectives may take turns on one workspace of
+ * the largest size that they ask for; a step of kfac.h needs one of its own (the
+ * policy loss keeps counters behind the flag word that have to be 0 between its
+ * calls, and a step would write over them: its statistics would then not be
+ * written).  Differences: matrices are row-major with a
  * row stride in elements (`ld` >= the width), and a pointer needs the
  * alignment of its element type only.  Nothing is allocated and no host
  * synchronisation is made, so every call may be captured into a graph.

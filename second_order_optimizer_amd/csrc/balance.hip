@@ -636,7 +636,7 @@ struct Regions {
 };
 Regions regions(int64_t tokens, int32_t E) {
   Regions r;
-  r.p = kFlagBytes;
+  r.p = kRegions;
   r.c = r.p + align_up(sizeof(float) * kBalanceBlocks * static_cast<size_t>(E), 256);
   r.z = r.c + align_up(sizeof(int32_t) * kBalanceBlocks * static_cast<size_t>(E), 256);
   r.n = r.z + align_up(sizeof(double) * kBalanceBlocks, 256);

@@ -207,7 +207,6 @@ __device__ inline RowScalars row_scalars(const TokArgs& a, const PolArgs& p, int
 // arrived, so no cache has to be written back (a release fence in every
 // workgroup does that: 2047 x 50001 bf16 92 -> 103 us).  A kernel of its own
 // for these sums took 4 us and a launch.
-constexpr int kArriveGroup = 32, kArriveStride = 64;      // counters 256 bytes apart
 
 __device__ inline bool counted_last(uint32_t* counter, uint32_t of) {
   if (__hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != of - 1) return false;
@@ -785,18 +784,14 @@ kfac_status_t run_preference(const TokArgs& a, const PrefArgs& q, RowStats rs, h
   return KFAC_OK;
 }
 
-// Workspace behind the flag word.  policy: part [kMaxPartials][3] double, the
-// counters.  preference: part [pairs][4] double, stat [rows] float2, wide [rows] double,
-// coef [rows] float.
-constexpr size_t kPolicyParts = kFlagBytes + sizeof(double) * 3 * kMaxPartials;
-constexpr size_t kArriveBytes = sizeof(uint32_t) * kArriveStride * (1 + kMaxPartials / kArriveGroup);
-static_assert(kPolicyParts % 256 == 0 && kArriveBytes % 256 == 0 && kMaxPartials % kArriveGroup == 0);
+// Regions.  policy: part [kMaxPartials][3] double.  preference: part [pairs][4]
+// double, stat [rows] float2, wide [rows] double, coef [rows] float.
 struct PrefRegions {
   size_t part, stat, wide, coef, end;
 };
 PrefRegions pref_regions(int64_t rows, int32_t pairs) {
   PrefRegions r;
-  r.part = kFlagBytes;
+  r.part = kRegions;
   r.stat = r.part + align_up(static_cast<size_t>(pairs) * 4 * sizeof(double), 256);
   r.wide = r.stat + align_up(static_cast<size_t>(rows) * sizeof(float2), 256);
   r.coef = r.wide + align_up(static_cast<size_t>(rows) * sizeof(double), 256);
@@ -807,7 +802,7 @@ PrefRegions pref_regions(int64_t rows, int32_t pairs) {
 }  // namespace
 
 size_t token_workspace_bytes(int objective, int64_t rows, int32_t groups) {
-  if (objective == KFAC_OBJ_POLICY) return kPolicyParts + kArriveBytes;
+  if (objective == KFAC_OBJ_POLICY) return kRegions + sizeof(double) * 3 * kMaxPartials;
   if (objective == KFAC_OBJ_PREFERENCE) return pref_regions(rows, groups).end;
   return kFlagBytes;
 }
@@ -835,12 +830,12 @@ kfac_status_t launch_policy(const kfac_token_rows_t& t, const kfac_policy_t& p, 
   q.weight = p.weight;
   q.old_logp = p.old_logp;
   q.ref = p.ref_logp;
-  q.part = reinterpret_cast<uint64_t*>(ws + kFlagBytes);
+  q.part = reinterpret_cast<uint64_t*>(ws + kRegions);
   q.lo = static_cast<float>(1.0 - static_cast<double>(p.clip_low));
   q.hi = static_cast<float>(1.0 + static_cast<double>(p.clip_high));
   q.kl = p.kl_coef;
   q.stats = p.stats;
-  q.arrived = reinterpret_cast<uint32_t*>(ws + kPolicyParts);
+  q.arrived = reinterpret_cast<uint32_t*>(ws + kFlagBytes);
   q.w0 = static_cast<float>(1.0 / static_cast<double>(t.rows));
   if (t.dtype == KFAC_BF16) pick_policy<__bf16>(a, q, st);
   else pick_policy<float>(a, q, st);

@@ -1,8 +1,11 @@
 """The objectives on the GPU beside their numbers: batches of nothing, workspaces, autograd and flags."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
+import second_order_optimizer_amd as K
 from tests.test_gpu_objectives import DT, U, gpu, near
 
 pytestmark = pytest.mark.gpu
@@ -27,3 +30,60 @@ def test_no_rows_of_any_length(Q, vocab, dtype):
     stats, seq, logp, grad = op.run(x, lab, torch.zeros(7, dtype=torch.int32, device="cuda"))
     near(stats, np.array([np.log(2), 0, 0, 1]), 4 * U)
     assert not seq.any() and logp.shape == (0,) and grad.shape == (0, vocab) and op.flags() == 0
+
+
+class Shared:
+    """C calls on one workspace, zeroed once."""
+    def __init__(self, Q, nbytes):
+        self.Q, self.lib = Q, Q._library()
+        self.buf = torch.zeros(nbytes + 256, dtype=torch.uint8, device="cuda")
+        self.ws, self.n = (self.buf.data_ptr() + 255) // 256 * 256, nbytes
+
+    def call(self, fn, *structs):
+        assert fn(*[ctypes.byref(s) for s in structs], self.ws, self.n, torch.cuda.current_stream().cuda_stream) == K.KFAC_OK
+
+    def rows(self, x, labels):
+        self.logp, self.grad = torch.empty(x.shape[0], device="cuda"), torch.empty_like(x)
+        return self.Q.TokenRows(logits=x.data_ptr(), labels=labels.data_ptr(), logp=self.logp.data_ptr(),
+                                grad=self.grad.data_ptr(), rows=x.shape[0], ld=x.shape[1], grad_ld=x.shape[1],
+                                vocab=x.shape[1], dtype=K.F32, label_type=self.Q.I64, logit_scale=1.0, grad_scale=1.0)
+
+    def policy(self, x, labels, adv):
+        stats = torch.full((4,), float("nan"), device="cuda")
+        self.call(self.lib.kfac_policy_loss, self.rows(x, labels),
+                  self.Q.Policy(advantage=adv.data_ptr(), stats=stats.data_ptr(), clip_low=0.2, clip_high=0.2))
+        return stats, self.logp, self.grad
+
+    def preference(self, x, labels, offsets):
+        seq, stats = torch.empty(offsets.numel() - 1, device="cuda"), torch.empty(4, device="cuda")
+        self.call(self.lib.kfac_preference_loss, self.rows(x, labels),
+                  self.Q.Preference(offsets=offsets.data_ptr(), seq=seq.data_ptr(), stats=stats.data_ptr(),
+                                    pairs=seq.numel() // 2, beta=0.1))
+        return stats, seq, self.logp, self.grad
+
+    def balance(self, x, chosen):
+        tokens, E = x.shape
+        counts = torch.empty(E, dtype=torch.int32, device="cuda")
+        prob, stats, grad = torch.empty(E, device="cuda"), torch.empty(4, device="cuda"), torch.empty_like(x)
+        self.call(self.lib.kfac_balance_loss,
+                  self.Q.Balance(logits=x.data_ptr(), chosen=chosen.data_ptr(), counts=counts.data_ptr(),
+                                 prob=prob.data_ptr(), stats=stats.data_ptr(), grad=grad.data_ptr(), tokens=tokens, ld=E,
+                                 grad_ld=E, experts=E, top_k=chosen.shape[1], dtype=K.F32, index_type=self.Q.I64, coef=0.01,
+                                 z_coef=1e-3, grad_scale=1.0))
+        return stats, counts, prob, grad
+
+
+def test_objectives_in_turn_on_one_workspace(Q):
+    """Other objectives between two policy losses on the same workspace leave its counters alone."""
+    x, router = torch.randn(3000, 1500, device="cuda"), torch.randn(9000, 256, device="cuda")
+    lab, adv = torch.randint(0, 1500, (3000,), device="cuda"), torch.randn(3000, device="cuda")
+    off, ids = gpu([0, 1000, 3000], torch.int32), torch.randint(0, 256, (9000, 2), device="cuda")
+    want = (Q.PolicyLoss(3000, 1500, "f32").run(x, lab, adv), Q.PreferenceLoss(3000, 1, 1500, "f32").run(x, lab, off),
+            Q.BalanceLoss(9000, 256, 2, "f32", z_coef=1e-3).run(router, ids))
+    s = Shared(Q, max(Q.workspace_size(Q.OBJ_POLICY, 3000), Q.workspace_size(Q.OBJ_PREFERENCE, 3000, 1),
+                      Q.workspace_size(Q.OBJ_BALANCE, 9000, 256)))
+    for turn in range(2):
+        for other in range(1, 3):
+            got = s.preference(x, lab, off) if other == 1 else s.balance(router, ids)
+            assert all(torch.equal(a, b) for a, b in zip(want[other], got)), (turn, other)
+            assert all(torch.equal(a, b) for a, b in zip(want[0], s.policy(x, lab, adv))), (turn, other)
