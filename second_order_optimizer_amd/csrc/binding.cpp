@@ -197,6 +197,13 @@ void take_rows(const Call& c, kfac_token_rows_t& t, PyObject* logits, PyObject* 
   t.labels = c.indices(labels, "labels", t.rows, -1, &t.label_type);
 }
 
+// The caller's output tensor has been written: operations that saved it for a
+// backward pass find out, as after torch's own writes in place.  (A tensor of
+// inference mode cannot be saved, and counts no writes.)
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // The caller's gradient tensor, checked, or none.
 at::Tensor given_grad(const Call& c, PyObject* o, int64_t rows, int64_t cols, int64_t* ld) {
   if (o == Py_None) return at::Tensor();
@@ -234,13 +241,15 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.ref_logp = c.floats(a[6], "ref_logp", t.rows);
     if (a[6] == Py_None && p.kl_coef > 0.f) c.refuse("kl_coef > 0 needs ref_logp");
     at::Tensor grad = given_grad(c, a[7], t.rows, t.vocab, &t.grad_ld);
+    const bool given = grad.defined();
     void* stream = c.enter();
     at::Tensor stats = c.make(4), logp = c.make(t.rows);
-    if (!grad.defined()) grad = c.make_rows(t.rows, t.vocab, t.ld, &t.grad_ld);
+    if (!given) grad = c.make_rows(t.rows, t.vocab, t.ld, &t.grad_ld);
     t.logp = logp.data_ptr<float>();
     t.grad = grad.data_ptr();
     p.stats = stats.data_ptr<float>();
     done(entries.policy_loss(&t, &p, plan->base.ws, plan->base.ws_bytes, stream), "kfac_policy_loss");
+    if (given) written(grad);
     return tuple_of({stats, logp, grad});
   });
 }
@@ -258,14 +267,16 @@ PyObject* preference_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.ref_logp = c.floats(a[4], "ref_logp", t.rows);
     p.pair_weight = c.floats(a[5], "pair_weight", p.pairs);
     at::Tensor grad = given_grad(c, a[6], t.rows, t.vocab, &t.grad_ld);
+    const bool given = grad.defined();
     void* stream = c.enter();
     at::Tensor stats = c.make(4), seq = c.make(seqs), logp = c.make(t.rows);
-    if (!grad.defined()) grad = c.make_rows(t.rows, t.vocab, t.ld, &t.grad_ld);
+    if (!given) grad = c.make_rows(t.rows, t.vocab, t.ld, &t.grad_ld);
     t.logp = logp.data_ptr<float>();
     t.grad = grad.data_ptr();
     p.seq = seq.data_ptr<float>();
     p.stats = stats.data_ptr<float>();
     done(entries.preference_loss(&t, &p, plan->base.ws, plan->base.ws_bytes, stream), "kfac_preference_loss");
+    if (given) written(grad);
     return tuple_of({stats, seq, logp, grad});
   });
 }
@@ -280,14 +291,16 @@ PyObject* balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     b.chosen = c.indices(a[2], "chosen", b.tokens, b.top_k, &b.index_type);
     b.mask = a[3] == Py_None ? nullptr : static_cast<const uint8_t*>(c.vector(a[3], "mask", b.tokens, at::kBool));
     at::Tensor grad = given_grad(c, a[4], b.tokens, b.experts, &b.grad_ld);
+    const bool given = grad.defined();
     void* stream = c.enter();
     at::Tensor stats = c.make(4), counts = c.make(b.experts, at::kInt), prob = c.make(b.experts);
-    if (!grad.defined()) grad = c.make_rows(b.tokens, b.experts, b.ld, &b.grad_ld);
+    if (!given) grad = c.make_rows(b.tokens, b.experts, b.ld, &b.grad_ld);
     b.stats = stats.data_ptr<float>();
     b.counts = counts.data_ptr<int32_t>();
     b.prob = prob.data_ptr<float>();
     b.grad = grad.data_ptr();
     done(entries.balance_loss(&b, plan->base.ws, plan->base.ws_bytes, stream), "kfac_balance_loss");
+    if (given) written(grad);
     return tuple_of({stats, counts, prob, grad});
   });
 }
@@ -309,10 +322,12 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
       c.matrix(y, "out", d.rows, d.cols, &d.y_ld);
     }
     if (a[6] != Py_None) d.offset_dev = static_cast<const int64_t*>(c.vector(a[6], "offset_tensor", 1, at::kLong));
+    const bool given = y.defined();
     void* stream = c.enter();
-    if (!y.defined()) y = c.make_rows(d.rows, d.cols, d.y_ld = d.cols, &d.y_ld);
+    if (!given) y = c.make_rows(d.rows, d.cols, d.y_ld = d.cols, &d.y_ld);
     d.y = y.data_ptr();
     done(entries.dropout(&d, stream), "kfac_dropout");
+    if (given) written(y);
     return THPVariable_Wrap(std::move(y));
   });
 }

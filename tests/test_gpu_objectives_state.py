@@ -87,3 +87,25 @@ def test_objectives_in_turn_on_one_workspace(Q):
             got = s.preference(x, lab, off) if other == 1 else s.balance(router, ids)
             assert all(torch.equal(a, b) for a, b in zip(want[other], got)), (turn, other)
             assert all(torch.equal(a, b) for a, b in zip(want[0], s.policy(x, lab, adv))), (turn, other)
+
+
+def test_writes_are_seen_by_autograd(Q):
+    """A tensor given to be written counts the write, so that a backward pass which saved it is refused."""
+    x, lab, f = torch.randn(4, 8, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda"), torch.ones(4, device="cuda")
+    off, ids = gpu([0, 2, 4], torch.int32), torch.zeros(4, 2, dtype=torch.int64, device="cuda")
+    calls = (lambda g: Q.PolicyLoss(4, 8, "f32").run(x, lab, f, grad=g),
+             lambda g: Q.PreferenceLoss(4, 1, 8, "f32").run(x, lab, off, grad=g),
+             lambda g: Q.BalanceLoss(4, 8, 2, "f32").run(x, ids, grad=g),
+             lambda g: Q.Dropout(4, 8, "f32").run(x, 1, out=g))
+    for call in calls:
+        g = torch.empty_like(x)
+        before = g._version
+        call(g)
+        assert g._version == before + 1 and x._version == 0
+        with torch.inference_mode():
+            g = torch.empty_like(x)
+        call(g)                               # outside the mode: written, nothing to count
+    h = torch.relu(torch.randn(4, 8, device="cuda", requires_grad=True))
+    Q.Dropout(4, 8, "f32", 0.5).run(h.detach(), 1, out=h.detach())
+    with pytest.raises(RuntimeError, match="inplace"):
+        h.sum().backward()
