@@ -38,20 +38,6 @@ ROWS, PAIRS, LENGTH = 512, 32, 8                   # 2 * PAIRS * LENGTH = ROWS: 
 HP = dict(lr=0.1, momentum=0.5, weight_decay=0.0, ema_decay=0.9, damping=1e-2)
 
 
-class Drop(torch.autograd.Function):
-    """The library's dropout as a node: the mask is made again in the backward pass."""
-
-    @staticmethod
-    def forward(ctx, x, op, seed, offset):
-        ctx.call = op, seed, offset
-        return op.run(x, seed, offset)
-
-    @staticmethod
-    def backward(ctx, dy):
-        op, seed, offset = ctx.call
-        return op.backward(dy.contiguous(), seed, offset), None, None, None
-
-
 class RoutedPolicy:
     def __init__(self, seed):
         gen = torch.Generator(device="cuda").manual_seed(seed)
@@ -79,7 +65,7 @@ class RoutedPolicy:
         h = torch.relu(pre)
         if train:
             self.passes += 1
-            h = Drop.apply(h, self.drop, self.seed, self.passes)
+            h = self.drop.run(h, self.seed, self.passes)      # the mask is made again in the backward pass
         z = torch.nn.functional.linear(h, *p[1])
         prob, expert = torch.softmax(z, 1).max(1)
         y = h * (1 + prob[:, None] * self.gain[expert])

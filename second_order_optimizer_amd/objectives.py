@@ -10,7 +10,8 @@ what stands on either side of an optimizer step and makes the rows it reads.
 Each class holds the shape, the constants and the workspace of one operator;
 ``run`` checks its tensors, allocates the outputs that are not given and makes
 one call into the library on the current (or the given) stream.  Losses return
-their gradients with the loss.  With the default weights (a mean over rows)
+their gradients with the loss; these and the log-probabilities are outside
+autograd (``logits.backward(grad)`` hands a gradient on), dropout is inside.  With the default weights (a mean over rows)
 and ``grad_scale=rows`` the gradients are per-row ones, the rows ``g`` that a
 ``KfacStack`` layer takes.  Argument marshalling only, as in the package: every
 operator runs in the library's HIP kernels and there is no fallback.  The
@@ -313,9 +314,32 @@ class BalanceLoss(_Operator):
         return self._on(stream, _native.balance_loss, logits, chosen, mask, grad)
 
 
+class _DropoutNode(torch.autograd.Function):
+    """Dropout's place in autograd: the backward pass is the same call on the output gradient."""
+
+    @staticmethod
+    def forward(ctx, x, residual, op, seed, offset, offset_tensor, stream):
+        y = op.run(x, seed, offset, residual, None, offset_tensor, stream)
+        ctx.call = op, seed, offset
+        ctx.save_for_backward(offset_tensor)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        op, seed, offset = ctx.call
+        offset_tensor, = ctx.saved_tensors
+        dx = op.backward(dy.contiguous(), seed, offset, None, offset_tensor) if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None, None, None, None
+
+
+def _tracked(t) -> bool:
+    return isinstance(t, torch.Tensor) and t.requires_grad
+
+
 class Dropout(_Operator):
     """Dropout whose mask is a function of (seed, offset, position): kept with probability 1 - p, scaled
-    by 1 / (1 - p) (p to 16 bits), nothing stored between forward and backward."""
+    by 1 / (1 - p) (p to 16 bits), nothing stored between forward and backward.  Where x or residual
+    requires grad, the result is part of autograd's graph."""
 
     def __init__(self, rows: int, cols: int, dtype: str = "bf16", p: float = 0.1, device="cuda"):
         super().__init__(_DropoutPlan(), dtype, device)
@@ -332,8 +356,13 @@ class Dropout(_Operator):
         seed, offset: 64-bit numbers that name the mask; a caller takes
         another offset for every layer and step.  offset_tensor: one int64 on
         the GPU, added to offset when the kernel runs (for captured graphs).
-        out: where to write; it may be x or residual itself.
+        out: where to write; it may be x or residual itself.  It is for
+        calls outside autograd: refused where x or residual requires grad.
         """
+        if (_tracked(x) or _tracked(residual)) and torch.is_grad_enabled():
+            if out is not None:
+                self._fail("out cannot be given where x or residual requires grad")
+            return _DropoutNode.apply(x, residual, self, seed, offset, offset_tensor, stream)
         if stream is None:
             return _native.dropout(self._at, x, seed, offset, residual, out, offset_tensor)
         return self._on(stream, _native.dropout, x, seed, offset, residual, out, offset_tensor)

@@ -109,3 +109,57 @@ def test_writes_are_seen_by_autograd(Q):
     Q.Dropout(4, 8, "f32", 0.5).run(h.detach(), 1, out=h.detach())
     with pytest.raises(RuntimeError, match="inplace"):
         h.sum().backward()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dropout_in_autograd(Q, dtype):
+    """The gradient of x is backward()'s of the output gradient, and the residual's is that itself; for any strides of
+    the output gradient, on a stream, and twice."""
+    op = Q.Dropout(9, 33, dtype, 0.3)
+    x, r, dy = (torch.randn(9, 33, device="cuda").to(DT[dtype]) for _ in range(3))
+    want, dx = op.run(x, 5, 6, residual=r), op.backward(dy, 5, 6)
+    xg, rg = x.clone().requires_grad_(), r.clone().requires_grad_()
+    y = op.run(xg, 5, 6, residual=rg)
+    assert torch.equal(y, want) and y.requires_grad
+    a, b = torch.autograd.grad(y, (xg, rg), dy)
+    assert torch.equal(a, dx) and torch.equal(b, dy)
+    assert torch.equal(torch.autograd.grad(op.run(xg, 5, 6), xg, dy.t().contiguous().t())[0], dx)
+    ones = torch.autograd.grad(op.run(xg, 5, 6, residual=r).float().sum(), xg)[0]          # a broadcast output gradient
+    assert torch.equal(ones, op.backward(torch.ones_like(x), 5, 6))
+    assert torch.equal(torch.autograd.grad(op.run(x, 5, 6, residual=rg), rg, dy)[0], dy)
+    # linear: the gradient's gradient is the same mask again
+    v = torch.ones_like(x, requires_grad=True)
+    g, = torch.autograd.grad(op.run(xg, 5, 6), xg, v, create_graph=True)
+    assert torch.equal(torch.autograd.grad(g, v, dy)[0], dx)
+    with torch.no_grad():
+        assert not op.run(xg, 5, 6).requires_grad
+    assert not op.run(xg.detach(), 5, 6).requires_grad
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = op.run(xg, 5, 6, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(torch.autograd.grad(y, xg, dy)[0], dx)
+
+
+def test_dropout_gradient_against_differences(Q):
+    """Linear in x: half the difference of two values along a direction is the gradient's product with it, up to the
+    roundings of those values (2 u each, over 297 entries)."""
+    op = Q.Dropout(9, 33, "f32", 0.3)
+    x, d, dy = (torch.randn(9, 33, device="cuda", dtype=torch.float64).float() for _ in range(3))
+    xg = x.clone().requires_grad_()
+    g = torch.autograd.grad(op.run(xg, 5, 6), xg, dy)[0].double()
+    up, down = op.run(x + d, 5, 6).double(), op.run(x - d, 5, 6).double()
+    lim = 4 * U * (dy.double().abs() * (up.abs() + down.abs())).sum() + 4 * U * (g * d.double()).abs().sum()
+    assert abs((g * d.double()).sum() - ((up - down) / 2 * dy.double()).sum()) <= lim
+
+
+def test_dropout_backward_sees_a_moved_offset(Q):
+    """A mask that offset_tensor named is found again in the backward pass, or that pass is refused."""
+    op = Q.Dropout(9, 33, "f32", 0.3)
+    x, step = torch.randn(9, 33, device="cuda", requires_grad=True), torch.full((1,), 4, dtype=torch.int64, device="cuda")
+    y = op.run(x, 5, 6, offset_tensor=step)
+    dy = torch.ones_like(x)
+    assert torch.equal(torch.autograd.grad(y, x, dy, retain_graph=True)[0], op.backward(dy, 5, 10))
+    step.add_(1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        torch.autograd.grad(y, x, dy)
