@@ -43,7 +43,8 @@ enum { KFAC_I32 = 0, KFAC_I64 = 1 };
 /* sticky flag, beside those of kfac.h: a label, an expert number or a
  * sequence offset beyond its range (that row, slot or sequence is then left
  * out, nothing is read or written out of bounds).  KFAC_FLAG_NONFINITE: a row
- * that counts has a loss or a gradient that is not finite. */
+ * that counts has a loss or a gradient that is not finite, or the losses' sum
+ * is not, in float32. */
 enum { KFAC_FLAG_BAD_INDEX = 4u };
 /* kfac_objective_workspace_size objectives */
 enum { KFAC_OBJ_LOGP = 0, KFAC_OBJ_POLICY = 1, KFAC_OBJ_PREFERENCE = 2, KFAC_OBJ_BALANCE = 3 };

@@ -346,6 +346,7 @@ __device__ inline void grad_tokens(const BalArgs& a, const Columns<S>& cols, Tok
   const uint32_t tokens = static_cast<uint32_t>(a.tokens);
   const int64_t grad_step = static_cast<int64_t>(at.stride) * a.ldg;
   char* grad = a.g + static_cast<int64_t>(at.t) * a.ldg;
+  bool bad = false;
   for (; at.t - slot < tokens; at.t += at.stride, grad += grad_step) {
     const uint32_t t = at.t;
     const TokenBack<S> cur = in;
@@ -363,6 +364,7 @@ __device__ inline void grad_tokens(const BalArgs& a, const Columns<S>& cols, Tok
     pf = group_reduce<S::LPT, false>(pf);
     const bool live = inv != 0.f;
     const float shift = (zs != 0.f ? zs * fmaf(__builtin_amdgcn_logf(inv), -kLn2, m) : 0.f) - pf;
+    bad |= live && !finite(shift);      // also where an f is not: its column is in pf
     if (t >= tokens) continue;
 #pragma unroll
     for (int q = 0; q < S::NV; ++q) {
@@ -375,6 +377,7 @@ __device__ inline void grad_tokens(const BalArgs& a, const Columns<S>& cols, Tok
       }
     }
   }
+  if (bad && (threadIdx.x & (S::LPT - 1)) == 0) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
 }
 
 // Factors of a count in f and of lse in the gradient, and the statistics.
@@ -393,7 +396,7 @@ struct Scales {
     a.stats[1] = static_cast<float>(balance);
     a.stats[2] = static_cast<float>(z);
     a.stats[3] = static_cast<float>(live);
-    if (!(fabs(balance + z) < INFINITY)) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
+    if (!(finite(a.stats[0]) && finite(a.stats[1]) && finite(a.stats[2]))) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
   }
 };
 

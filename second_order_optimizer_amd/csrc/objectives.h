@@ -111,6 +111,8 @@ __device__ inline float max3(float a, float b, float c) {
   return d;
 }
 
+__device__ inline bool finite(float v) { return fabsf(v) < INFINITY; }
+
 // v from the lane that the DPP control names (all controls used here have a
 // source inside the same 16 lanes).
 template <int CTRL>

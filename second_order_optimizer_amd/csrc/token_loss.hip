@@ -215,7 +215,7 @@ __device__ inline bool counted_last(uint32_t* counter, uint32_t of) {
 }
 
 template <int TEAMS>
-__device__ inline void policy_stats(const PolArgs& p, const double (*sums)[3], int* last) {
+__device__ inline void policy_stats(const PolArgs& p, uint32_t* flags, const double (*sums)[3], int* last) {
   if (threadIdx.x == 0) {
     uint64_t* q = p.part + static_cast<int64_t>(blockIdx.x) * 3;
     for (int k = 0; k < 3; ++k) {
@@ -247,10 +247,12 @@ __device__ inline void policy_stats(const PolArgs& p, const double (*sums)[3], i
   if (threadIdx.x == 0) {
     double t[3];
     for (int k = 0; k < 3; ++k) t[k] = (red[0][k] + red[1][k]) + (red[2][k] + red[3][k]);
-    p.stats[0] = static_cast<float>(p.kl != 0.f ? t[0] + static_cast<double>(p.kl) * t[1] : t[0]);
+    const float loss = static_cast<float>(p.kl != 0.f ? t[0] + static_cast<double>(p.kl) * t[1] : t[0]);
+    p.stats[0] = loss;
     p.stats[1] = static_cast<float>(t[0]);
     p.stats[2] = static_cast<float>(t[1]);
     p.stats[3] = static_cast<float>(t[2]);
+    if (!finite(loss)) raise_flag(flags, KFAC_FLAG_NONFINITE);      // a sum of finite rows may pass float32
   }
 }
 
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
         acc_a -= static_cast<double>(cur.w) * gain;
         acc_k += static_cast<double>(cur.w) * kl;
         acc_c += clipped ? cur.w : 0.f;
-        bad |= !(fabsf(gain) < INFINITY && fabsf(kl) < INFINITY && fabsf(o.neg) < INFINITY);
+        bad |= !(finite(gain) && finite(kl) && finite(o.neg));
         return o;
       };
       Softmax r = wave_softmax<FINE>(t, c, clo);
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
     if (bad) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
   }
   __syncthreads();
-  policy_stats<TEAMS>(p, sums, &last);
+  policy_stats<TEAMS>(p, a.flags, sums, &last);
 }
 
 // ---------------------------------------------------------------------------
@@ -588,10 +590,10 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a
       q[1] = h > 0.0 ? w : 0.0;
       q[2] = w != 0.0 ? w * beta * h : 0.0;
       q[3] = w;
-      bool bad = w != 0.0 && !(fabs(loss) < INFINITY);
+      bool bad = !finite(static_cast<float>(q[0]));
       for (int k = 0; k < 2; ++k) {
         coef[k] = w != 0.0 ? static_cast<float>((k ? -w : w) * slope * share[k] * static_cast<double>(a.grad_scale)) : 0.f;
-        bad |= !(fabsf(coef[k]) < INFINITY);
+        bad |= !finite(coef[k]);
       }
       if (bad) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
     }
@@ -647,7 +649,10 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) preference_grad_kerne
         double t = 0.0;
         for (int i = threadIdx.x; i < p.pairs; i += kWave) t += p.part[static_cast<int64_t>(i) * 4 + q];
         t = wave_sum(t);
-        if (threadIdx.x == 0) p.stats[q] = static_cast<float>(t);
+        if (threadIdx.x == 0) {
+          p.stats[q] = static_cast<float>(t);
+          if (q == 0 && !finite(p.stats[0])) raise_flag(a.flags, KFAC_FLAG_NONFINITE);
+        }
       }
     }
     return;

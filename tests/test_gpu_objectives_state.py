@@ -163,3 +163,47 @@ def test_dropout_backward_sees_a_moved_offset(Q):
     step.add_(1)
     with pytest.raises(RuntimeError, match="inplace"):
         torch.autograd.grad(y, x, dy)
+
+
+# -- results beyond float32 --------------------------------------------------------------------
+
+def test_policy_sum_beyond_float32_is_flagged(Q):
+    """Rows whose losses are finite and whose sum is not."""
+    x, lab = torch.zeros(4, 8, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
+    op = Q.PolicyLoss(4, 8, "f32", grad_scale=1e-3)
+    w = torch.ones(4, device="cuda")
+    stats, _, grad = op.run(x, lab, torch.full((4,), 2e38, device="cuda"), weight=w)
+    assert stats[0].isinf() and grad.isfinite().all() and op.flags(clear=True) == K.FLAG_NONFINITE
+    assert op.run(x, lab, torch.full((4,), 2e37, device="cuda"), weight=w)[0].isfinite().all() and op.flags() == 0
+
+
+def test_preference_loss_beyond_float32_is_flagged(Q):
+    x, lab, off = torch.zeros(2, 8, device="cuda"), gpu([2, 3]), gpu([0, 1, 2], torch.int32)
+    op = Q.PreferenceLoss(2, 1, 8, "f32", kind="squared")
+    stats, _, _, grad = op.run(x, lab, off, ref_logp=gpu([-1e25, 0], torch.float32))
+    assert stats[0].isinf() and grad.isfinite().all() and op.flags(clear=True) == K.FLAG_NONFINITE
+    assert op.run(x, lab, off, ref_logp=gpu([-1e15, 0], torch.float32))[0].isfinite().all() and op.flags() == 0
+
+
+def test_preference_sum_beyond_float32_is_flagged(Q):
+    """Pairs whose losses are finite and whose sum is not."""
+    x, lab, off = torch.zeros(8, 8, device="cuda"), gpu(np.arange(8)), gpu(np.arange(9), torch.int32)
+    op = Q.PreferenceLoss(8, 4, 8, "f32", kind="squared")
+    ref = gpu([-1.4e19] * 4 + [0.0] * 4, torch.float32)
+    stats = op.run(x, lab, off, ref_logp=ref, pair_weight=torch.ones(4, device="cuda"))[0]
+    assert stats[0].isinf() and op.flags() == K.FLAG_NONFINITE
+
+
+@pytest.mark.parametrize("tokens,E", [(40, 16), (9000, 256)])
+def test_balance_beyond_float32_is_flagged(Q, tokens, E):
+    """A z loss, a gradient of it and a gradient of the balance loss that float32 does not hold, in one launch and in
+    three; masked tokens that would are not looked at."""
+    ids = torch.zeros(tokens, 1, dtype=torch.int64, device="cuda")
+    for fill, kw in ((1e25, dict(z_coef=1e-3)), (100.0, dict(z_coef=1e3, grad_scale=2e34 * tokens)),
+                     (0.0, dict(coef=1e30, grad_scale=1e20))):
+        x = torch.full((tokens, E), fill, device="cuda")
+        op = Q.BalanceLoss(tokens, E, 1, "f32", **kw)
+        stats, _, _, grad = op.run(x, ids)
+        assert not (stats.isfinite().all() and grad.isfinite().all()) and op.flags(clear=True) == K.FLAG_NONFINITE, kw
+        stats, _, _, grad = op.run(x, ids, mask=torch.zeros(tokens, dtype=torch.bool, device="cuda"))
+        assert not stats.any() and not grad.any() and op.flags() == 0, kw
