@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
         if (cur.w == 0.f) return o;
         const float ratio = p.old_logp ? expf(o.logp - cur.old_logp) : 1.f;
         const float held = fminf(fmaxf(ratio, p.lo), p.hi);
-        const float first = ratio * cur.adv, second = held * cur.adv;
+        // an advantage of 0 is a term of 0, also where the ratio passes float32
+        const float first = cur.adv != 0.f ? ratio * cur.adv : 0.f, second = held * cur.adv;
         const bool clipped = second < first;
         const float gain = clipped ? second : first;
         float slope = clipped ? 0.f : -first, kl = 0.f;

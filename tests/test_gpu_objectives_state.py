@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import second_order_optimizer_amd as K
+from oracle import objectives as O
 from tests.test_gpu_objectives import DT, U, gpu, near
 
 pytestmark = pytest.mark.gpu
@@ -207,3 +208,16 @@ def test_balance_beyond_float32_is_flagged(Q, tokens, E):
         assert not (stats.isfinite().all() and grad.isfinite().all()) and op.flags(clear=True) == K.FLAG_NONFINITE, kw
         stats, _, _, grad = op.run(x, ids, mask=torch.zeros(tokens, dtype=torch.bool, device="cuda"))
         assert not stats.any() and not grad.any() and op.flags() == 0, kw
+
+
+@pytest.mark.parametrize("vocab", [8, 3001])
+def test_zero_advantage_with_a_ratio_beyond_float32(Q, vocab):
+    """A term of 0 and a gradient of 0, not 0 times infinity; a positive advantage there is clipped."""
+    x = torch.zeros(2, vocab, device="cuda")
+    x[:, 0] = 200.0
+    adv, old = np.array([0.0, 1.0]), np.array([-100.0, -100.0])
+    op = Q.PolicyLoss(2, vocab, "f32")
+    stats, _, grad = op.run(x, gpu([0, 0]), gpu(adv, torch.float32), old_logp=gpu(old, torch.float32))
+    want = O.policy_loss(x.cpu().numpy(), [0, 0], adv, None, old, hi=float(np.float32(0.2)))[0]
+    near(stats, want, 4 * U * np.abs(want))
+    assert not grad.any() and op.flags() == 0
