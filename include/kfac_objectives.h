@@ -118,7 +118,7 @@ typedef struct kfac_preference {
   const float* pair_weight;  /* [pairs], NULL: 1 / pairs */
   float* seq;                /* [2 pairs], written: R */
   float* stats;              /* [4], written: loss, sum w [h > 0], sum w beta h, sum w */
-  int32_t pairs;             /* >= 1 */
+  int32_t pairs;             /* 1 .. 2^22 - 1; rows <= 2^31 - 1 */
   int32_t kind;              /* KFAC_PREF_SIGMOID | KFAC_PREF_SQUARED */
   float beta;                /* > 0 */
   float label_smoothing;     /* 0 <= e < 0.5 (sigmoid) */

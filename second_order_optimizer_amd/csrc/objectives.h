@@ -19,6 +19,7 @@ constexpr int kArriveStride = 64;         // words between counters
 constexpr size_t kArriveBytes = sizeof(uint32_t) * kArriveStride * (1 + kMaxPartials / kArriveGroup);
 constexpr size_t kRegions = kFlagBytes + kArriveBytes;
 static_assert(kRegions % 256 == 0 && kMaxPartials % kArriveGroup == 0);
+constexpr int kPairThreads = 1024;        // preference: threads of a pair's workgroup
 constexpr int kBalanceMaxExperts = 1024;
 constexpr int64_t kDropoutMaxBlocks = (int64_t(1) << 32) - 1024;  // generator blocks a call
 constexpr int kBalanceBlocks = 512;       // balance: workgroups of the first pass

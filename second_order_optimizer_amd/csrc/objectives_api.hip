@@ -67,7 +67,8 @@ kfac_status_t kfac_objective_workspace_size(int32_t objective, int64_t rows, int
     case KFAC_OBJ_POLICY: break;
     case KFAC_OBJ_PREFERENCE:
       if (groups < 1) return KFAC_ERR_ARG;
-      if (groups >= (1 << 30) || rows > INT32_MAX) return KFAC_ERR_UNSUPPORTED;
+      // one launch covers 2^32 - 1 threads
+      if (static_cast<int64_t>(groups) * kfac::kPairThreads > UINT32_MAX || rows > INT32_MAX) return KFAC_ERR_UNSUPPORTED;
       break;
     case KFAC_OBJ_BALANCE:
       if (groups < 1) return KFAC_ERR_ARG;

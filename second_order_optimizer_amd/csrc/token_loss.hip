@@ -508,8 +508,6 @@ struct PrefArgs {
   float beta, eps, w0;
 };
 
-constexpr int kPairThreads = 1024;
-
 __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a, PrefArgs p) {
   constexpr int WAVES = kPairThreads / kWave;
   static_assert(WAVES == 16, "row_sum adds 16 lanes");

@@ -1,4 +1,6 @@
-"""What the objectives' classes refuse of autograd, on the host."""
+"""Further refusals of the objectives, on the host: what belongs to autograd, and sizes past one launch."""
+import ctypes
+
 import pytest
 import torch
 
@@ -18,3 +20,19 @@ def test_dropout_refuses_out_where_a_gradient_is_wanted():
             with torch.no_grad(), pytest.raises(K.KfacError) as e:
                 op.run(seed=1, out=out, **kw)
             assert e.value.status == K.KFAC_ERR_UNSUPPORTED        # as far as a GPU is needed
+
+
+def test_pairs_past_one_launch_are_refused():
+    """A workgroup of 1024 threads a pair: from 2^22 pairs a launch has more than 2^32 - 1 threads, and would fail
+    after the log-probabilities were enqueued."""
+    lib = Q._library()
+    rows = Q.TokenRows(logits=0x10000, labels=0x20000, logp=0x30000, grad=0x40000, rows=4, ld=16, grad_ld=16, vocab=16,
+                       dtype=K.BF16, label_type=Q.I64, logit_scale=1.0, grad_scale=1.0)
+    for pairs in (1 << 22, (1 << 22) + 1, (1 << 30) - 1, 1 << 30):
+        with pytest.raises(K.KfacError) as e:
+            Q.workspace_size(Q.OBJ_PREFERENCE, 4, pairs)
+        assert e.value.status == K.KFAC_ERR_UNSUPPORTED, pairs
+        pref = Q.Preference(offsets=0x60000, seq=0x63000, stats=0x64000, pairs=pairs, beta=0.1)
+        st = lib.kfac_preference_loss(ctypes.byref(rows), ctypes.byref(pref), 0x100000, 1 << 40, None)
+        assert st == K.KFAC_ERR_UNSUPPORTED, pairs
+    assert Q.workspace_size(Q.OBJ_PREFERENCE, 4, (1 << 22) - 1) > 1 << 27
