@@ -33,8 +33,8 @@ struct TokArgs {
   int32_t vocab;
   int32_t label_type;
   float scale;         // s
-  float c;             // s log2(e): exp(s d) = 2^(c d)
-  float clo;           // what c leaves of s log2(e)
+  float c, clo;        // s log2(e): exp(s d) = 2^(c d + clo d)
+  float near;          // the same to the nearest float32
   float grad_scale;    // s grad_scale
   uint32_t* flags;
 };
@@ -60,9 +60,14 @@ struct Softmax {
 // FINE multiplies by s log2(e) to twice float32's width: c alone is off by up
 // to 3e-8 of itself, which biases log S by that times the mean exponent, the
 // same way in every row; sums of log-probabilities over a sequence would show
-// it.  bf16 gradients do without.
+// it.  bf16 gradients, and the policy loss's bf16 rows, do without: their c is
+// the nearest float32, so that log S is off by at most 6e-8 times the mean
+// exponent (the float below the product, which the pair needs, may be twice as
+// far: 1.25 and 0.85 are such scales).
 template <typename T>
 constexpr bool kFine = sizeof(T) == 4;
+template <typename T>
+__device__ inline float scale_of(const TokArgs& a) { return kFine<T> ? a.c : a.near; }
 template <bool FINE>
 __device__ inline float exp_of(float d, float c, float clo) {
   return __builtin_amdgcn_exp2f(FINE ? fmaf(d, c, d * clo) : d * c);
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
   const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM), tid = threadIdx.x % TEAM;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
   const int nfull = a.vocab / VE, ntail = a.vocab % VE;
-  const float c = a.c, clo = a.clo;
+  const float c = scale_of<T>(a), clo = a.clo;
   constexpr bool FINE = kFine<T>;
 
   u32x4 v[NV];
@@ -632,7 +637,7 @@ __device__ inline void grad_row(const TokArgs& a, const char* x, char* g, int ti
       const int idx = (j0 + j) * TEAM + tid;
       if (idx < nfull)
         store16<NTS>(g + static_cast<int64_t>(idx) * 16,
-                     zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(u[j], m, a.c, a.clo, neg));
+                     zero ? u32x4{0u, 0u, 0u, 0u} : grad_vec<T>(u[j], m, scale_of<T>(a), a.clo, neg));
     }
   }
 }
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) preference_grad_kerne
     else grad_row<T, TEAM, UN, false, NT>(a, x, g, tid, ms.x, neg, zero);
     if (tid < ntail) {
       const int64_t e = static_cast<int64_t>(nfull) * VE + tid;
-      Elem<T>::store(g, e, zero ? 0.f : grad_one<T>(Elem<T>::load(x, e), ms.x, a.c, a.clo, neg));
+      Elem<T>::store(g, e, zero ? 0.f : grad_one<T>(Elem<T>::load(x, e), ms.x, scale_of<T>(a), a.clo, neg));
     }
     if (!zero) {
       const int lv = label / VE;
@@ -700,7 +705,7 @@ TokArgs tok_args(const kfac_token_rows_t& t, char* ws) {
   a.label_type = t.label_type;
   a.scale = t.logit_scale;
   const double c = static_cast<double>(t.logit_scale) * 1.4426950408889634;
-  a.c = static_cast<float>(c);
+  a.c = a.near = static_cast<float>(c);
   // c below the exact product and clo above 0, so that a difference of minus
   // infinity stays one in d c + d clo
   if (static_cast<double>(a.c) >= c) a.c = std::nextafter(a.c, 0.f);

@@ -221,3 +221,18 @@ def test_zero_advantage_with_a_ratio_beyond_float32(Q, vocab):
     want = O.policy_loss(x.cpu().numpy(), [0, 0], adv, None, old, hi=float(np.float32(0.2)))[0]
     near(stats, want, 4 * U * np.abs(want))
     assert not grad.any() and op.flags() == 0
+
+
+def test_policy_logp_has_no_bias_from_the_rounded_scale(Q):
+    """bf16 rows multiply by s log2(e) in float32.  At s = 0.85 the nearest float32 is 0.04 u from it, its lower
+    neighbour 1.6 u: over the mean exponent of 8.5 here that one would bias log S by 13 u.  The roundings of the
+    products (64 values of the logits, up to 11 u each, of either sign) leave less than 3 u of their mean, log S of
+    1.8 and its float32 another 2 u."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    x = (-10 - 4 * torch.rand(64, 131072, generator=gen, device="cuda")).bfloat16()
+    x[:, 0] = 0
+    op = Q.PolicyLoss(64, 131072, logit_scale=0.85)
+    logp = op.run(x, torch.zeros(64, dtype=torch.int64, device="cuda"), torch.ones(64, device="cuda"))[1]
+    want = -torch.logsumexp(x.double() * float(np.float32(0.85)), 1)
+    assert abs((logp.double() - want).mean()) <= 5 * U
+
