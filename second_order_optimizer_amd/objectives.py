@@ -187,8 +187,10 @@ class _Operator:
             return call(self._at, *args)
 
     def flags(self, clear: bool = False) -> int:
-        """The sticky flags (FLAG_NONFINITE, FLAG_BAD_INDEX); waits for the current stream."""
-        return read_flags(self.ws_ptr, clear)
+        """The sticky flags (FLAG_NONFINITE, FLAG_BAD_INDEX); waits for the current stream of the operator's
+        GPU (a call that was given another stream has to be waited for by the caller)."""
+        with torch.cuda.device(self.dev):
+            return read_flags(self.ws_ptr, clear)
 
 
 class _Tokens(_Operator):

@@ -36,3 +36,25 @@ def test_pairs_past_one_launch_are_refused():
         st = lib.kfac_preference_loss(ctypes.byref(rows), ctypes.byref(pref), 0x100000, 1 << 40, None)
         assert st == K.KFAC_ERR_UNSUPPORTED, pairs
     assert Q.workspace_size(Q.OBJ_PREFERENCE, 4, (1 << 22) - 1) > 1 << 27
+
+
+def test_flags_are_read_on_the_objects_device(monkeypatch):
+    """The stream that flags() waits for is the current one of the operator's GPU, not of the current GPU."""
+    op = Q.PolicyLoss(4, 8, dtype="f32", device="cpu")
+    op.dev = torch.device("cuda", 1)
+    here, seen = [0], []
+
+    class On:
+        def __init__(self, dev):
+            self.dev = torch.device(dev).index
+
+        def __enter__(self):
+            self.before, here[0] = here[0], self.dev
+
+        def __exit__(self, *exc):
+            here[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(Q, "read_flags", lambda ws, clear=False, stream=None: seen.append((here[0], ws, clear)) or 2)
+    assert op.flags(clear=True) == 2
+    assert seen == [(1, op.ws_ptr, True)] and here == [0]
