@@ -15,6 +15,7 @@
 #include <ATen/ATen.h>
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 
 #include <optional>
 #include <string>
@@ -305,13 +306,20 @@ PyObject* balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (plan, x, seed, offset, residual, out, offset_tensor) -> y
+// (plan, x, seed, offset, residual, out, offset_tensor) -> y, or None (and nothing
+// done) where the call belongs into autograd's graph
 PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const DropoutPlan* plan = plan_of<DropoutPlan>(a, n, 7);
     Call c(plan->base);
     kfac_dropout_t d = plan->d;
-    d.x = c.matrix(c.tensor(a[1], "x"), "x", d.rows, d.cols, &d.ld);
+    const at::Tensor& x = c.tensor(a[1], "x");
+    if (c10::GradMode::is_enabled() &&
+        (x.requires_grad() || (a[4] != Py_None && c.tensor(a[4], "residual").requires_grad()))) {
+      if (a[5] != Py_None) c.refuse("out cannot be given where x or residual requires grad");
+      Py_RETURN_NONE;
+    }
+    d.x = c.matrix(x, "x", d.rows, d.cols, &d.ld);
     d.seed = PyLong_AsUnsignedLongLongMask(a[2]);
     d.offset = PyLong_AsUnsignedLongLongMask(a[3]);
     if (PyErr_Occurred()) return nullptr;

@@ -334,10 +334,6 @@ class _DropoutNode(torch.autograd.Function):
         return dx, dy if ctx.needs_input_grad[1] else None, None, None, None, None, None
 
 
-def _tracked(t) -> bool:
-    return isinstance(t, torch.Tensor) and t.requires_grad
-
-
 class Dropout(_Operator):
     """Dropout whose mask is a function of (seed, offset, position): kept with probability 1 - p, scaled
     by 1 / (1 - p) (p to 16 bits), nothing stored between forward and backward.  Where x or residual
@@ -361,13 +357,13 @@ class Dropout(_Operator):
         out: where to write; it may be x or residual itself.  It is for
         calls outside autograd: refused where x or residual requires grad.
         """
-        if (_tracked(x) or _tracked(residual)) and torch.is_grad_enabled():
-            if out is not None:
-                self._fail("out cannot be given where x or residual requires grad")
-            return _DropoutNode.apply(x, residual, self, seed, offset, offset_tensor, stream)
         if stream is None:
-            return _native.dropout(self._at, x, seed, offset, residual, out, offset_tensor)
-        return self._on(stream, _native.dropout, x, seed, offset, residual, out, offset_tensor)
+            y = _native.dropout(self._at, x, seed, offset, residual, out, offset_tensor)
+        else:
+            y = self._on(stream, _native.dropout, x, seed, offset, residual, out, offset_tensor)
+        if y is None:           # x or residual requires grad, and autograd is on
+            return _DropoutNode.apply(x, residual, self, seed, offset, offset_tensor, stream)
+        return y
 
     def backward(self, dy, seed: int, offset: int = 0, out=None, offset_tensor=None, stream=None):
         """d loss / dx from d loss / dy, with the mask of run(x, seed, offset); the residual's gradient is dy."""
