@@ -27,7 +27,8 @@
  * tensors of dropout; everything else is float32 or an integer.  Gradients
  * are those of the objective times grad_scale: with a mean over rows and
  * grad_scale = rows they are per-row gradients, the rows g that
- * kfac_layer_t expects.
+ * kfac_layer_t expects.  That descriptor has no row stride: write them with
+ * grad_ld = the width, into the layer's buffer.
  */
 #ifndef KFAC_OBJECTIVES_H
 #define KFAC_OBJECTIVES_H
@@ -64,7 +65,8 @@ typedef struct kfac_token_rows {
   float* logp;          /* [rows], written */
   void* grad;           /* losses: [rows, vocab] of dtype, row stride grad_ld, written; may be `logits`
                            itself with grad_ld == ld, must not overlap it otherwise */
-  int64_t rows;         /* >= 0 (0: pointers may be NULL, stats are written as 0) */
+  int64_t rows;         /* >= 0 (0: pointers of [rows, ...] arrays may be NULL; the policy's stats
+                           are then 0, a preference pair counts with h = 0) */
   int64_t ld;
   int64_t grad_ld;
   int32_t vocab;        /* >= 1 */
@@ -89,7 +91,9 @@ typedef struct kfac_token_rows {
 typedef struct kfac_policy {
   const float* advantage;  /* [rows] */
   const float* weight;     /* [rows], NULL: 1 / rows */
-  const float* old_logp;   /* [rows], NULL: the policy's own, held fixed (ratio 1) */
+  const float* old_logp;   /* [rows], NULL: the policy's own, held fixed (ratio 1).  One that
+                              kfac_token_logp gave for the same logits makes a ratio that is 1
+                              up to float32 roundings of logp */
   const float* ref_logp;   /* [rows], NULL: no KL term (kl_coef must be 0) */
   float* stats;            /* [4], written: loss, sum w A, sum w K, sum w [clipped] */
   float clip_low;          /* 0 <= clip_low <= 1 */

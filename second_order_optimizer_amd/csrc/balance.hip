@@ -20,8 +20,8 @@
 // has out of the sums; both compute the same gradient there.  E below a vector:
 // one element a lane.
 //
-// 65536 tokens of 256 bf16 logits: first pass 14.1 us, sums 4.5 us (latency),
-// second pass 11.8 us, where a copy of the same 34 MB takes 10.3 us.  The first
+// 65536 tokens of 256 bf16 logits: first pass 14.0 us, sums 4.5 us (latency),
+// second pass 12.3 us, where a copy of the same 34 MB takes 10.3 us.  The first
 // pass issues some 115 vector operations for a lane's eight logits (6.7 us in
 // all; only 1 us of it the exponentials' own rate), the rest is the launch, the
 // first loads and the sums at the end.  The next token's logits are loaded while

@@ -54,9 +54,9 @@ __device__ inline void store16(void* p, u32x4 v) {
 
 // The memory-side cache.  Streams that fit it together find what was written
 // just before and leave theirs for what comes next; larger ones go past it
-// with nontemporal accesses.  Measured on large copies and reads: 5.5 TB/s
-// and 6.3 TB/s through the cache, 6.0 and 7.1 past it (128 MB copied again
-// and again: 8.2 through it, 6.4 past it).
+// with nontemporal accesses.  Measured on copies and reads of 2 GiB: 5.7 TB/s
+// and 6.4 TB/s through the cache, 6.2 and 7.2 past it (128 MiB copied again
+// and again: 7.0 through it, 6.2 past it).
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
 
 // Element type traits: VE elements per 16-byte vector.

@@ -175,12 +175,22 @@ __device__ inline float grad_one(float x, float m, float c, float clo, float neg
 // each gradient written once.  A team walks rows a grid apart and asks for
 // the next row's vector in the place of each one it has finished, so loads
 // and stores stay mixed and no phase waits for an empty pipe.  LONG: rows
-// beyond the registers (TEAM * NV vectors) read the rest twice.
+// beyond the registers (TEAM * NV vectors) read the rest twice (512 x 140003 bf16
+// 85 us, 1024 x 131072 f32 266: 53 and 75% of a row is read again).
 //
-// Bound by HBM with reads and writes mixed: 4096 x 131072 bf16 424 us, 5.1 TB/s
-// (a copy as large: 6.2); without the exponentials it is 2% less.  2047 x 50001
-// bf16 92 us, 4.4 TB/s: eight rows a compute unit, so the first loads and the
-// last stores, with nothing to pair them with, are a ninth each.
+// Bound by HBM with reads and writes mixed: 4096 x 131072 bf16 421 us for 2.07 GB
+// (the 7% of rows without a label are written, not read), 4.9 TB/s (a copy as
+// large: 6.2); without the exponentials it is 2% less.  2047 x 50001 bf16 92 us
+// for 0.39 GB, 4.3 TB/s: eight rows a compute unit, so the first loads and the
+// last stores, with nothing to pair them with, are a ninth each, which is some 8
+// of the 28 us over a copy's time; what the others are was not found.
+//
+// A row's scalars (logp, ratio, KL term, coefficient, coef / S) are float32,
+// formed from the 64-bit sum: logp is off by a few 2^-24 of its two terms, and the
+// ratio and the gradient by as much relatively (256 x 1000 f32: 2e-7 against 64
+// bits).  Their 64-bit functions are some hundred instructions each for a lane
+// that the row waits for.  For the same reason logp here and in logp_kernel,
+// which has them, differ in their last bits.
 
 struct RowScalars {
   int32_t label;
@@ -321,7 +331,8 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
         }
       }
       // what follows from the row's sum is the same for all of it: one wavefront
-      // works it out and the others wait (4096 x 12000 bf16 44.6 -> 43.1 us)
+      // works it out and the others wait (4096 x 12000 bf16 44.6 -> 43.1 us; 2047 x 50001
+      // 90.5 -> 92.1)
       auto terms = [&](Softmax r) {
         RowTerms o{r.m, 0.f, 0.f, log_prob(cur.xl, r, a.scale)};
         if (cur.w == 0.f) return o;
@@ -416,12 +427,12 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) policy_kernel(TokArgs
 // differences of it; with `stat` each row's (M, 1 / S) and with `wide` its logp
 // in 64 bits are kept for the kernels below.  Rows before `past` are read past
 // the cache.  Bound by HBM reads: 8192 x 32768 bf16 86 us, 6.2 TB/s; 1024 x
-// 131072 f32 81 us, 6.6 TB/s.  64 rows of 32768: 5 us, of which the launch is
-// half.  Wavefronts a row by the rows there are: 1024 threads where 256 would
+// 131072 f32 82 us, 6.5 TB/s (reads alone: 7.2).  64 rows of 32768: 5 us, of which
+// the launch is half.  Wavefronts a row by the rows there are: 1024 threads where 256 would
 // leave compute units idle.
 
 struct RowStats {
-  float2* stat;
+  float2* stat;        // 1 / S to float32: the gradient is off by 2^-24 of itself for it
   double* wide;
   float* coef;         // set to 0 for preference_pair_kernel
   int64_t past;
@@ -615,10 +626,10 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(TokArgs a
 // coefficient.  The rows are taken last to first: where logits and gradients
 // do not fit the cache, the first pass reads all but its last rows past it
 // and the gradients are stored past it, so that those last rows are still
-// there (the whole loss 287 -> 250 us on 7200 rows of 32768 bf16 logits, 243 now).  The
-// extra workgroup adds up the pairs' statistics.  Bound by memory: 165 us for
-// the 0.94 GB of these rows and gradients (5.7 TB/s), after 78 us of first pass
-// and 5 us between; the second read is the price of a coefficient that needs
+// there (the whole loss 287 -> 250 us on 7155 rows of 32768 bf16 logits, 243 now).  The
+// extra workgroup adds up the pairs' statistics.  Bound by memory: 161 us for
+// the 0.89 GB of gradients and of logits of rows with a label (5.5 TB/s), after 78
+// us of first pass and 5 us between; the second read is the price of a coefficient that needs
 // the whole pair.
 template <typename T, int TEAM, int UN, bool NTL, bool NTS>
 __device__ inline void grad_row(const TokArgs& a, const char* x, char* g, int tid, float m, float neg, bool zero) {
@@ -730,8 +741,8 @@ void run_policy(const TokArgs& a, const PolArgs& p, int per_cu, hipStream_t st) 
 // the row, a wavefront a row as far as 512 vectors (no barriers; 16384 x 500
 // bf16 with registers for 256 vectors instead of 64: 21.6 us against 17.3 us).
 // From 4096 vectors one row a workgroup and compute unit: two of half the size
-// would count 512 workgroups' sums in and load no faster (2047 x 50001 bf16 97
-// us, 103 with two).  Past 16384 vectors half of the registers hold the row's
+// would count 512 workgroups' sums in and load no faster (2047 x 50001 bf16 with
+// a label in every row 98 us, 103 with two).  Past 16384 vectors half of the registers hold the row's
 // start and the other half its stream: with more for the start they spill
 // (1024 x 131072 f32 272 us with 12 vectors, 262 with 8).
 template <typename T>

@@ -11,15 +11,19 @@ Each class holds the shape, the constants and the workspace of one operator;
 ``run`` checks its tensors, allocates the outputs that are not given and makes
 one call into the library on the current (or the given) stream.  Losses return
 their gradients with the loss; these and the log-probabilities are outside
-autograd (``logits.backward(grad)`` hands a gradient on), dropout is inside.  With the default weights (a mean over rows)
-and ``grad_scale=rows`` the gradients are per-row ones, the rows ``g`` that a
-``KfacStack`` layer takes.  Argument marshalling only, as in the package: every
-operator runs in the library's HIP kernels and there is no fallback.  The
-marshalling of a call is native (csrc/binding.cpp, the ``_objectives``
-extension).
+autograd (``logits.backward(grad)`` hands a gradient on), dropout is inside.
+With the default weights (a mean over rows) and ``grad_scale=rows`` the
+gradients are per-row ones, the rows ``g`` that a ``KfacStack`` layer takes.
+They are contiguous there: give the layer's buffer as ``grad``, or copy (a new
+gradient has the logits' row stride modulo 16 bytes).  Argument marshalling
+only, as in the package: every operator runs in the library's HIP kernels and
+there is no fallback.  The marshalling of a call is native (csrc/binding.cpp,
+the ``_objectives`` extension).
 
 One object is for one call at a time: calls on different streams or host
-threads take objects of their own.
+threads take objects of their own.  Its shape is fixed, and making one
+allocates and synchronises: keep one per shape.  A graph that captured its
+calls works in its workspace: keep the object as long as the graph.
 """
 from __future__ import annotations
 
@@ -258,8 +262,9 @@ class PreferenceLoss(_Tokens):
 
     rows: tokens of all sequences; the `pairs` preferred sequences come
     first, then the rejected ones in the same order.  kind: "sigmoid" (with
-    label_smoothing) or "squared".  average: log ratios are averaged over a
-    sequence's labelled tokens rather than summed.
+    label_smoothing) or "squared" (which has none, whatever is given).
+    average: log ratios are averaged over a sequence's labelled tokens rather
+    than summed.
     """
 
     def __init__(self, rows: int, pairs: int, vocab: int, dtype: str = "bf16", beta: float = 0.1,
