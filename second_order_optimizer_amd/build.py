@@ -1,5 +1,6 @@
 """Builds libkfac.so (the HIP kernels + C ABI) in-tree for gfx950 with hipcc, and
-the _objectives extension (calls of the objectives on torch tensors).
+the extensions with the calls on torch tensors: _objectives (objectives and
+dropout) and _tokens (sampling, embedding, orthogonalised updates).
 
 Usage: python -m second_order_optimizer_amd.build [-v]
 """
@@ -17,7 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkfac.so")
-EXT = os.path.join(PKG, "_objectives.so")
+EXTS = {"binding.cpp": os.path.join(PKG, "_objectives.so"), "binding_tokens.cpp": os.path.join(PKG, "_tokens.so")}
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # -packed-fp32-ops off: plain fp32 vector code, no packed-fp32 instructions.
@@ -37,8 +38,8 @@ def _run(cmd, verbose):
         print(out)
 
 
-def _build_extension(verbose) -> None:
-    """csrc/binding.cpp (host code only) against torch's and Python's headers."""
+def _build_extension(source, target, verbose) -> None:
+    """A csrc/binding*.cpp (host code only) against torch's and Python's headers."""
     import torch
     base = os.path.dirname(torch.__file__)
     rocm = os.path.dirname(os.path.dirname(HIPCC))
@@ -49,13 +50,13 @@ def _build_extension(verbose) -> None:
     for d in include:
         flags += ["-isystem", d]
     libs = ["-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
-    tmp = EXT + ".tmp"
-    _run([os.environ.get("CXX", "g++")] + flags + [os.path.join(CSRC, "binding.cpp"), "-o", tmp] + libs, verbose)
-    os.replace(tmp, EXT)
+    tmp = target + ".tmp"
+    _run([os.environ.get("CXX", "g++")] + flags + [os.path.join(CSRC, source), "-o", tmp] + libs, verbose)
+    os.replace(tmp, target)
 
 
 def build(verbose: bool = False, jobs: int = 8) -> str:
-    """Compiles every csrc/*.hip, links libkfac.so and builds the extension; returns the library's path."""
+    """Compiles every csrc/*.hip, links libkfac.so and builds the extensions; returns the library's path."""
     os.makedirs(OBJ, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     objs = [os.path.join(OBJ, os.path.basename(s)[:-4] + ".o") for s in srcs]
@@ -64,10 +65,11 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
         s, o = pair
         _run([HIPCC] + HIP_FLAGS + ["-c", s, "-o", o], verbose)
 
-    with ThreadPoolExecutor(max(1, min(jobs, len(srcs) + 1))) as ex:
-        ext = ex.submit(_build_extension, verbose)
+    with ThreadPoolExecutor(max(1, min(jobs, len(srcs) + len(EXTS)))) as ex:
+        exts = [ex.submit(_build_extension, s, t, verbose) for s, t in EXTS.items()]
         list(ex.map(cc, zip(srcs, objs)))
-        ext.result()
+        for e in exts:
+            e.result()
     tmp = LIB + ".tmp"
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs, verbose)
     os.replace(tmp, LIB)

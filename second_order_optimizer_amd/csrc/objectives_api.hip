@@ -1,39 +1,13 @@
 // The extern "C" entry points of include/kfac_objectives.h: host-side
 // validation and dispatch.
 #include "objectives.h"
+#include "validate.h"
 
 #include <cmath>
 
 namespace kfac {
 
 namespace {
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Pointers that are dereferenced: present, and aligned to their element.
-struct Ptrs {
-  kfac_status_t s = KFAC_OK;
-  void need(const void* p, size_t align) {
-    if (s == KFAC_OK && !p) s = KFAC_ERR_ARG;
-    else may(p, align);
-  }
-  void may(const void* p, size_t align) {
-    if (s == KFAC_OK && p && !aligned(p, align)) s = KFAC_ERR_ALIGN;
-  }
-};
-
-bool dtype_ok(int32_t d) { return d == KFAC_F32 || d == KFAC_BF16; }
-size_t elem_size(int32_t d) { return d == KFAC_BF16 ? 2 : 4; }
-bool index_ok(int32_t t) { return t == KFAC_I32 || t == KFAC_I64; }
-size_t index_size(int32_t t) { return t == KFAC_I64 ? 8 : 4; }
-
-// rows x ld elements must have byte offsets of at most 62 bits.
-bool extent_ok(int64_t rows, int64_t ld) { return rows == 0 || ld <= (INT64_MAX / 8) / rows; }
-
-kfac_status_t check_workspace(const void* ws, size_t have, size_t need) {
-  if (!ws || have < need) return KFAC_ERR_WORKSPACE;
-  return aligned(ws, 256) ? KFAC_OK : KFAC_ERR_ALIGN;
-}
 
 kfac_status_t check_rows(const kfac_token_rows_t* t, bool grad) {
   if (!t || t->reserved != 0) return KFAC_ERR_ARG;

@@ -154,7 +154,8 @@ _DTYPES = {"bf16": (BF16, torch.bfloat16), "f32": (F32, torch.float32)}
 class _Operator:
     """Shape, device and workspace shared by the operators."""
 
-    def __init__(self, plan, dtype: str, device, objective: Optional[int] = None, rows: int = 0, groups: int = 0):
+    def __init__(self, plan, dtype: str, device, objective: Optional[int] = None, rows: int = 0, groups: int = 0,
+                 ws_bytes: Optional[int] = None):
         self._where = type(self).__name__
         if dtype not in _DTYPES:
             self._fail("dtype must be 'bf16' or 'f32'", KFAC_ERR_DTYPE)
@@ -167,7 +168,9 @@ class _Operator:
         self.ws_ptr = self.ws_bytes = 0
         tensor = home = None
         if objective is not None:
-            self.ws_bytes = workspace_size(objective, rows, groups)
+            ws_bytes = workspace_size(objective, rows, groups)
+        if ws_bytes is not None:
+            self.ws_bytes = ws_bytes
             self._ws = torch.zeros(self.ws_bytes + 256, dtype=torch.uint8, device=dev)
             self.ws_ptr = (self._ws.data_ptr() + 255) // 256 * 256
             if dev.type == "cuda":      # the workspace may be used on any stream from here on

@@ -1,0 +1,213 @@
+"""Orthogonalised updates on the GPU against the float64 oracle.
+
+Tolerance: oracle.orthogonal.error_bound, the worst that rounding the
+iteration's matrices to 11 (products "half") or 22 bits ("full") can do to the
+result's 2-norm, with the outputs' own half step on top.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import orthogonal as O
+from tests.test_gpu_objectives import DT, HALF, U, wide
+
+pytestmark = pytest.mark.gpu
+BITS = {"half": 11, "full": 22}
+
+
+@pytest.fixture()
+def M(gpu_lib):
+    from second_order_optimizer_amd import orthogonal
+    return orthogonal
+
+
+def draw(rng, rows, cols, dtype="f32", rank=3):
+    x = rng.normal(size=(rows, cols)) + 2 * rng.normal(size=(rows, rank)) @ rng.normal(size=(rank, cols))
+    t = torch.from_numpy((1e-3 * x).astype(np.float32)).to(DT[dtype]).cuda()
+    return t, wide(t)
+
+
+def check(got, x, dtype, products, **kw):
+    want = O.orthogonalize(x, **kw)
+    off = np.linalg.norm(wide(got) - want)
+    tol = O.error_bound(x, BITS[products], **kw) + HALF[dtype] * np.linalg.norm(want)
+    assert off <= tol, (off, tol, np.linalg.norm(want))
+    return off / max(np.linalg.norm(want), 1e-30)
+
+
+SHAPES = [(1, 1), (1, 7), (7, 1), (2, 3), (5, 5), (16, 64), (64, 33), (64, 64), (65, 65), (127, 128), (129, 128), (128, 500),
+          (300, 129), (255, 257), (32, 1000), (1000, 32), (513, 700), (900, 1025)]
+
+
+@pytest.mark.parametrize("dtype,products", [("bf16", None), ("f32", None), ("f32", "half"), ("bf16", "full")])
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_orthogonalize(M, rows, cols, dtype, products):
+    x, xd = draw(np.random.default_rng(rows * 31 + cols), rows, cols, dtype)
+    op = M.Orthogonal(rows, cols, dtype=dtype, products=products)
+    got = op.run(x)
+    assert got.shape == x.shape and got.dtype == x.dtype
+    off = check(got, xd, dtype, products or ("half" if dtype == "bf16" else "full"))
+    print(rows, cols, dtype, products, off)
+    assert op.flags() == 0 and torch.equal(got, op.run(x))
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(2049, 2300, "bf16"), (2500, 2100, "f32"), (1024, 3500, "bf16")])
+def test_orthogonalize_large(M, rows, cols, dtype):
+    x, xd = draw(np.random.default_rng(rows), rows, cols, dtype)
+    print(check(M.Orthogonal(rows, cols, dtype=dtype).run(x), xd, dtype, "half" if dtype == "bf16" else "full"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_batches_and_strides(M, dtype):
+    """A batch is its matrices one by one; rows and matrices any stride apart; out given, and x itself."""
+    rng = np.random.default_rng(3)
+    whole = torch.from_numpy(rng.normal(size=(5, 40, 150)).astype(np.float32)).to(DT[dtype]).cuda()
+    x = whole[:, 3:36, 11:140]
+    batch, rows, cols = x.shape
+    op, one = M.Orthogonal(rows, cols, batch, dtype), M.Orthogonal(rows, cols, dtype=dtype)
+    got = op.run(x)
+    for i in range(batch):
+        check(got[i], wide(x[i]), dtype, "half" if dtype == "bf16" else "full")
+        assert torch.equal(got[i], one.run(x[i]))
+    room = torch.full((5, 50, 200), 7.0, dtype=DT[dtype], device="cuda")
+    out = room[:, 5:38, 21:150]
+    assert op.run(x, out=out).data_ptr() == out.data_ptr() and torch.equal(out, got)
+    room[:, 5:38, 21:150] = 7.0
+    assert (room == 7.0).all()
+    before = whole.clone()
+    op.run(x, out=x)
+    assert torch.equal(x, got)
+    whole[:, 3:36, 11:140] = before[:, 3:36, 11:140]
+    assert torch.equal(whole, before)
+    assert M.Orthogonal(rows, cols, 0, dtype).run(torch.empty(0, rows, cols, dtype=DT[dtype], device="cuda")).shape[0] == 0
+
+
+def test_steps_and_coefficients(M):
+    """One step and sixteen, a triple a step, a cubic, and what is no contraction."""
+    x, xd = draw(np.random.default_rng(4), 100, 160)
+    for coefs, steps in ((O.COEFS, 1), (O.COEFS, 3), ((1.5, -0.5, 0.0), 16), ((1.875, -1.25, 0.375), 9),
+                         (((3.0, -3.5, 1.4), (2.6, -2.6, 0.9), (2.0, -1.5, 0.5)), 3), ((1.0, 0.0, 0.0), 2)):
+        for products in ("half", "full"):
+            got = M.Orthogonal(100, 160, dtype="f32", steps=steps, coefs=coefs, products=products).run(x)
+            check(got, xd, "f32", products, coefs=coefs, steps=steps)
+    # values up to 1 can become 1.33 in the first step, 1.36 (with 2%) becomes 2.3, that 100, and that 5e9: refused
+    with pytest.raises(RuntimeError) as e:
+        M.Orthogonal(100, 160, steps=4, coefs=((4.0, -6.0, 2.7), (3.9, -6.0, 2.6), (3.5, -5.0, 2.2), (2.0, -1.5, 0.5)))
+    assert e.value.status == 5
+
+
+def test_values_that_are_far_apart(M):
+    """Tiny and huge matrices, zeros, one entry, one huge row: the norm is 64-bit and the scale is the matrix's."""
+    rng = np.random.default_rng(5)
+    base = rng.normal(size=(70, 90)).astype(np.float32)
+    op = M.Orthogonal(70, 90, dtype="f32", eps=0.0)
+    for scale in (1e-38, 1e-20, 1.0, 1e20, 1e37):
+        x = torch.from_numpy(base * np.float32(scale)).cuda()
+        check(op.run(x), wide(x), "f32", "full", eps=0.0)
+    assert (op.run(torch.zeros(70, 90, device="cuda")) == 0).all() and op.flags() == 0
+    for where in ((0, 0), (69, 89)):
+        x = torch.zeros(70, 90, device="cuda")
+        x[where] = -3.0
+        check(op.run(x), wide(x), "f32", "full", eps=0.0)
+    x = torch.from_numpy(base).cuda()
+    x[5] *= 1e4
+    check(op.run(x), wide(x), "f32", "full", eps=0.0)
+
+
+def test_flags(M, gpu_lib):
+    for v in (np.nan, np.inf):
+        op = M.Orthogonal(40, 40, 2, dtype="f32")
+        x = torch.randn(2, 40, 40, device="cuda")
+        want = op.run(x)[0]
+        x[1, 3, 4] = v
+        got = op.run(x)
+        assert op.flags(clear=True) == gpu_lib.FLAG_NONFINITE
+        assert torch.equal(got[0], want) and not torch.isfinite(got[1]).any()
+        x[1, 3, 4] = 0
+        op.run(x)
+        assert op.flags() == 0
+
+
+def stack(rng, shapes, biases):
+    f = lambda *s: torch.from_numpy(rng.normal(size=s).astype(np.float32)).cuda()  # noqa: E731
+    w, m, g = ([f(*s) for s in shapes] for _ in range(3))
+    b, bm, bg = ([f(s[0]) if has else None for s, has in zip(shapes, biases)] for _ in range(3))
+    return w, m, g, b, bm, bg
+
+
+@pytest.mark.parametrize("nesterov,scale,products", [(True, "aspect", "full"), (False, "rms", "full"), (True, "none", "half")])
+def test_step(M, nesterov, scale, products):
+    """Two steps of a stack of more layers than a launch holds, of all shapes, some without a bias."""
+    rng = np.random.default_rng(8)
+    shapes = [(32, 64), (64, 32), (1, 5), (5, 1), (130, 129), (257, 40)] + [(10 + i, 50 - i) for i in range(20)]
+    w, m, g, b, bm, bg = stack(rng, shapes, [i % 3 != 1 for i in range(len(shapes))])
+    op = M.OrthogonalStep(w, m, b, bm, nesterov=nesterov, scale=scale, products=products)
+    lr, mu, wd = 0.05, 0.9, 0.02
+    for _ in range(2):
+        was = [[None if t is None else wide(t) for t in v] for v in (w, m, b, bm)]
+        versions = [t._version for t in w]
+        op.run(g, bg, lr=lr, momentum=mu, weight_decay=wd)
+        assert all(t._version > v for t, v in zip(w, versions))
+        for i, (rows, cols) in enumerate(shapes):
+            gd = wide(g[i])
+            ww, wm = O.step(was[0][i], was[1][i], gd, lr, mu, wd, nesterov=nesterov, scale=scale)
+            assert (np.abs(wide(m[i]) - wm) <= 2 * U * (np.abs(gd) + np.abs(was[1][i]))).all()
+            u = gd + mu * wm if nesterov else wm
+            tol = lr * O.shape_factor(rows, cols, scale) * (O.error_bound(u, BITS[products]) + 4 * U * np.linalg.norm(O.orthogonalize(u)))
+            assert np.linalg.norm(wide(w[i]) - ww) <= tol + 4 * U * np.linalg.norm(was[0][i]), i
+            if b[i] is not None:
+                wb, wbm = O.bias_step(was[2][i], was[3][i], wide(bg[i]), lr, mu, wd)
+                size = np.abs(wide(bg[i])) + np.abs(was[3][i]) + np.abs(was[2][i])
+                assert (np.abs(wide(bm[i]) - wbm) <= 4 * U * size).all() and (np.abs(wide(b[i]) - wb) <= 4 * U * size).all()
+    assert op.flags() == 0
+
+
+def test_step_on_a_stack(M):
+    """On the state of a KfacStack, between its own steps' buffers."""
+    from types import SimpleNamespace
+    from second_order_optimizer_amd.stack import KfacStack
+    rng = np.random.default_rng(2)
+    st = KfacStack([SimpleNamespace(kind="linear", d_in=64, d_out=32, has_bias=True, rows=8)], "full")
+    s, inp = st.state[0], st.inputs[0][0]
+    for t in (s["w"], inp["grad_w"], inp["grad_b"]):
+        t.copy_(torch.from_numpy(rng.normal(size=t.shape)))
+    was, g = wide(s["w"]), wide(inp["grad_w"])
+    M.OrthogonalStep([s["w"]], [s["mom_w"]], [s["b"]], [s["mom_b"]]).run([inp["grad_w"]], [inp["grad_b"]], lr=0.1)
+    want, _ = O.step(was, np.zeros_like(was), g, 0.1, 0.95, 0.0)
+    assert np.linalg.norm(wide(s["w"]) - want) <= 0.1 * O.error_bound(g, 22) + 8 * U * np.linalg.norm(was)
+
+
+def test_captured_and_replayed(M):
+    """A step and an update in one graph, replayed on other gradients, against eager steps of another stack."""
+    rng = np.random.default_rng(11)
+    shapes = [(140, 70), (33, 200)]
+    w, m, g, b, bm, bg = stack(rng, shapes, [True, True])
+    x = torch.randn(3, 50, 60, device="cuda").bfloat16()
+    copy = lambda v: [t.clone() for t in v]  # noqa: E731
+    w2, m2, b2, bm2 = copy(w), copy(m), copy(b), copy(bm)
+    one, two = M.OrthogonalStep(w, m, b, bm), M.OrthogonalStep(w2, m2, b2, bm2)
+    o1, o2 = M.Orthogonal(50, 60, 3), M.Orthogonal(50, 60, 3)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one.run(g, bg)
+        y = o1.run(x)
+    for _ in range(4):
+        for t in (*g, *bg, x):
+            t.normal_()
+        graph.replay()
+        two.run(g, bg)
+        want = o2.run(x)
+        torch.cuda.synchronize()
+        for u, v in zip((*w, *m, *b, *bm, y), (*w2, *m2, *b2, *bm2, want)):
+            assert torch.equal(u, v)
+
+
+def test_on_another_stream(M):
+    x = torch.randn(300, 200, device="cuda")
+    op = M.Orthogonal(300, 200, dtype="f32")
+    want = op.run(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = op.run(x, stream=s)
+    s.synchronize()
+    assert torch.equal(want, got)
