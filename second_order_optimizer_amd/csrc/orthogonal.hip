@@ -40,8 +40,9 @@ typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kNormBlocks = 256;      // partial sums of a matrix's squares
-constexpr int kMaxProbs = 16;         // problems a launch
+constexpr int kNormBlocks = 1024;     // most partial sums of a matrix's squares
+constexpr int kMaxProbs = 14;         // problems a launch
+constexpr int kBand = 4;              // tile rows whose tiles of a column run together
 
 __device__ inline void split(float v, f16& hi, f16& lo) {
   hi = static_cast<f16>(v);
@@ -62,7 +63,7 @@ struct PrepProb {
   f16* same;            // planes laid out as x, [rows_p, cols_p]
   f16* turned;          // [cols_p, rows_p]
   int64_t plane, same_stride, turned_stride;
-  int32_t rows_p, cols_p, tiles_c, blk2_begin, tall;
+  int32_t rows_p, cols_p, tiles_c, blk2_begin;
   float scale;          // power of two
 };
 struct PrepBatch {
@@ -81,8 +82,29 @@ __device__ inline int find(const PrepBatch& b, int blk) {
   return i;
 }
 
-__device__ inline float load_any(const void* p, int64_t i, int bf16) {
-  return bf16 ? bf16_bits_to_float(static_cast<const unsigned short*>(p)[i]) : static_cast<const float*>(p)[i];
+// 8 values of a row from column c on, those past its `cols` columns 0.
+__device__ inline void load8(float (&f)[8], const void* row, int c, int cols, int bf16) {
+  if (c + 8 <= cols) {
+    if (bf16) {
+      const u32x4 v = load16(static_cast<const unsigned short*>(row) + c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = Elem<__bf16>::get(v, e);
+    } else {
+      const u32x4 v0 = load16(static_cast<const float*>(row) + c), v1 = load16(static_cast<const float*>(row) + c + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(e < 4 ? v0[e & 3] : v1[e & 3]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      f[e] = c + e >= cols ? 0.f
+             : bf16        ? bf16_bits_to_float(static_cast<const unsigned short*>(row)[c + e])
+                           : static_cast<const float*>(row)[c + e];
+  }
+}
+__device__ inline const void* row_at(const PrepProb& P, int64_t at) {
+  return P.bf16 ? static_cast<const void*>(static_cast<const unsigned short*>(P.x) + at)
+                : static_cast<const void*>(static_cast<const float*>(P.x) + at);
 }
 // The matrix that is orthogonalised, from a gradient and its momentum after the update.
 __device__ inline float direction(const PrepBatch& b, float g, float m) { return b.nesterov ? fmaf(b.mu, m, g) : m; }
@@ -92,20 +114,36 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(PrepBatch b) {
   const PrepProb& P = b.p[find<0>(b, blockIdx.x)];
   const int t = blockIdx.x - P.blk_begin;
   const int mat = t / P.blocks, blk = t % P.blocks;
-  const int64_t base = mat * P.stride;
   double sum = 0.0;
-  for (int r = blk; r < P.rows; r += P.blocks) {
-    for (int c = threadIdx.x; c < P.cols; c += 256) {
-      float u = load_any(P.x, base + r * P.ld + c, P.bf16);
-      if (P.mom) {
-        float* m = P.mom + static_cast<int64_t>(r) * P.cols + c;
-        const float v = fmaf(b.mu, *m, u);
-        *m = v;
-        u = direction(b, u, v);
+  const int per_row = (P.cols + 7) / 8;
+  const int64_t vectors = static_cast<int64_t>(P.rows) * per_row;
+  for (int64_t i = static_cast<int64_t>(blk) * 256 + threadIdx.x; i < vectors; i += static_cast<int64_t>(P.blocks) * 256) {
+    const int r = static_cast<int>(i / per_row), c = static_cast<int>(i - static_cast<int64_t>(r) * per_row) * 8;
+    float u[8];
+    load8(u, row_at(P, mat * P.stride + r * P.ld), c, P.cols, P.bf16);
+    if (P.mom) {
+      float* at = P.mom + static_cast<int64_t>(r) * P.cols;
+      float m[8];
+      load8(m, at, c, P.cols, 0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        m[e] = fmaf(b.mu, m[e], u[e]);
+        u[e] = direction(b, u[e], m[e]);
       }
-      sum += static_cast<double>(u) * static_cast<double>(u);
+      if (c + 8 <= P.cols) {
+        store16(at + c, pack16<float>(m));
+        store16(at + c + 4, pack16<float>(m + 4));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < P.cols) at[c + e] = m[e];
+      }
     }
-    if (P.bias && threadIdx.x == 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fma(static_cast<double>(u[e]), static_cast<double>(u[e]), sum);
+  }
+  if (P.bias) {
+    for (int r = blk * 256 + threadIdx.x; r < P.rows; r += P.blocks * 256) {
       const float v = fmaf(b.mu, P.bias_mom[r], fmaf(b.wd, P.bias[r], P.bias_grad[r]));
       P.bias_mom[r] = v;
       P.bias[r] = fmaf(-b.lr, v, P.bias[r]);
@@ -119,7 +157,7 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(PrepBatch b) {
 
 // -- second pass: the normalised matrix in planes, both ways round ---------------
 
-// With HALF the low halves are stored with X alone.
+// With HALF the low halves are stored of the matrix as x lies, not of the turned one.
 template <int PLANES>
 __global__ void __launch_bounds__(256) orth_load_kernel(PrepBatch b) {
   __shared__ float tile[64][65];
@@ -131,7 +169,8 @@ __global__ void __launch_bounds__(256) orth_load_kernel(PrepBatch b) {
   t -= mat * tiles;
   const int r0 = t / P.tiles_c * 64, c0 = t % P.tiles_c * 64;
   const int tid = threadIdx.x;
-  double sum = tid < P.blocks ? P.part[static_cast<int64_t>(mat) * kNormBlocks + tid] : 0.0;
+  double sum = 0.0;
+  for (int i = tid; i < P.blocks; i += 256) sum += P.part[static_cast<int64_t>(mat) * kNormBlocks + i];
   sum = wave_sum(sum);
   if ((tid & 63) == 0) red[tid / 64] = sum;
   __syncthreads();
@@ -139,31 +178,50 @@ __global__ void __launch_bounds__(256) orth_load_kernel(PrepBatch b) {
   if (!(sum < INFINITY) && t == 0 && tid == 0) raise_flag(b.flags, KFAC_FLAG_NONFINITE);
   const double norm = sqrt(sum) + b.eps;
   const double inv = norm > 0.0 ? static_cast<double>(P.scale) / norm : 0.0;
-  const int64_t base = mat * P.stride;
   f16* same = P.same + mat * P.same_stride;
   f16* turned = P.turned + mat * P.turned_stride;
-  for (int i = tid; i < 64 * 64; i += 256) {
-    const int r = r0 + i / 64, c = c0 + i % 64;
-    float u = 0.f;
+  const int tr = tid / 8, tc = tid % 8 * 8;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = r0 + tr + 32 * h, c = c0 + tc;
+    float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (r < P.rows && c < P.cols) {
-      u = load_any(P.x, base + r * P.ld + c, P.bf16);
-      if (P.mom) u = direction(b, u, P.mom[static_cast<int64_t>(r) * P.cols + c]);
-      u = static_cast<float>(static_cast<double>(u) * inv);
+      load8(u, row_at(P, mat * P.stride + r * P.ld), c, P.cols, P.bf16);
+      if (P.mom) {
+        float m[8];
+        load8(m, P.mom + static_cast<int64_t>(r) * P.cols, c, P.cols, 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = direction(b, u[e], m[e]);
+      }
     }
-    tile[i / 64][i % 64] = u;
-    f16 hi, lo;
-    split(u, hi, lo);
+    f16x8 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      u[e] = static_cast<float>(static_cast<double>(u[e]) * inv);
+      f16 x, y;
+      split(u[e], x, y);
+      hi[e] = x;
+      lo[e] = y;
+      tile[tr + 32 * h][tc + e] = u[e];
+    }
     const int64_t at = static_cast<int64_t>(r) * P.cols_p + c;
-    same[at] = hi;
-    if (PLANES == 2 || !P.tall) same[P.plane + at] = lo;
+    *reinterpret_cast<f16x8*>(same + at) = hi;
+    *reinterpret_cast<f16x8*>(same + P.plane + at) = lo;
   }
   __syncthreads();
-  for (int i = tid; i < 64 * 64; i += 256) {
-    f16 hi, lo;
-    split(tile[i % 64][i / 64], hi, lo);
-    const int64_t at = static_cast<int64_t>(c0 + i / 64) * P.rows_p + r0 + i % 64;
-    turned[at] = hi;
-    if (PLANES == 2 || P.tall) turned[P.plane + at] = lo;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    f16x8 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f16 x, y;
+      split(tile[tc + e][tr + 32 * h], x, y);
+      hi[e] = x;
+      lo[e] = y;
+    }
+    const int64_t at = static_cast<int64_t>(c0 + tr + 32 * h) * P.rows_p + r0 + tc;
+    *reinterpret_cast<f16x8*>(turned + at) = hi;
+    if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(turned + P.plane + at) = lo;
   }
 }
 
@@ -175,58 +233,131 @@ struct GemmProb {
   int64_t a_plane, b_plane, c_plane, o_plane, ot_plane;
   int64_t a_batch, b_batch, c_batch, o_batch, ot_batch;
   int32_t lda, ldb, ldo, ldot;      // c is laid out as o
-  int32_t k, tn, tiles, sym, blk_begin;
+  int32_t k, tm, tn, tiles, blk_begin;      // tiles of a matrix; the first of all
+  int64_t unit_begin;                       // the first stage of all
   float s_acc, s_c;           // result = s_acc P Q^T + s_c C
-  float *d_out, *d_in;        // HALF: the diagonal that the result leaves out, and the one that P left out
-  int64_t d_batch;
+  float *d_out, *d_in;        // HALF: the diagonal that the result leaves out, and the one that B left out,
+  int32_t d_batch, d_cols;    // a value a row of C, or a column
   // last product: the update goes to y, or into w
   void* y;
   float* w;
   int64_t y_ld, y_batch;
-  int32_t rows, cols, tall, y_bf16;
+  int32_t rows, cols, y_bf16;
   float decay, factor;
 };
+// Workgroups take whole tiles (units 0), or equal shares of all tiles' stages one
+// after the other: `units` stages over the grid's workgroups.  A share that is not
+// a whole tile goes to `partial`, place 2 w for the tile it begins in and 2 w + 1 for
+// the one it ends in, and the join kernel adds a tile's shares in order.
 struct GemmBatch {
   GemmProb p[kMaxProbs];
   int32_t n;
+  int32_t workgroups;       // of the shares
+  int64_t units;
+  float* partial;
 };
 static_assert(sizeof(GemmBatch) <= 4096, "kernel arguments");
 
-#define KFAC_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 0xF) | (0x7 << 4) | (0xF << 8))
+// s_waitcnt with only the vector-memory counter limited to n (n < 64)
+#define KFAC_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 0xF) | (((n) >> 4) << 14) | (0x7 << 4) | (0xF << 8))
 
-template <int PLANES, int BT, bool LAST>
-__global__ void __launch_bounds__(BT == 256 ? 512 : 256) orth_gemm_kernel(GemmBatch batch) {
-  constexpr int THREADS = BT == 256 ? 512 : 256;
-  constexpr int BK = PLANES == 2 ? 32 : 64;           // contraction a stage
-  constexpr int CHUNKS = BK / 8;                      // 16-byte chunks of a row
-  constexpr int OP = BT * BK;                         // elements of an operand's plane of a stage
-  constexpr int LOADS = OP / 8 / THREADS;             // loads a thread and plane
-  constexpr int MI = BT == 256 ? 4 : 2, NJ = 2;       // 32 x 32 blocks of a wavefront
-  __shared__ __attribute__((aligned(16))) f16 ring[2][2][PLANES][OP];
-  int pi = 0;
-  while (pi + 1 < batch.n && batch.p[pi + 1].blk_begin <= static_cast<int>(blockIdx.x)) ++pi;
-  const GemmProb& P = batch.p[pi];
-  int t = blockIdx.x - P.blk_begin;
-  const int mat = t / P.tiles;
-  t -= mat * P.tiles;
-  int ti, tj;
-  if (P.sym) {                       // upper tiles, row by row
-    ti = 0;
-    int width = P.tn;
-    while (t >= width) { t -= width; --width; ++ti; }
-    tj = ti + t;
-  } else {
-    ti = t / P.tn;
-    tj = t % P.tn;
+// instruction classes of __builtin_amdgcn_sched_group_barrier
+constexpr int kSchedMfma = 0x008;
+constexpr int kSchedDsRead = 0x100;
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+__device__ inline f16x8 turned_rows(const f16* a, const f16* b) {
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)a);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)b);
+  return __builtin_bit_cast(f16x8, s16x8(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)));
+}
+
+// What a product is for, and with it what its epilogue does.
+enum Kind { kGram, kPoly, kNext, kLast, kWeight };      // A; B; X; O; the weight that takes O
+
+// A kernel's tile: BM x BN, the contraction BK a stage, SLOTS stages in LDS, wavefronts
+// of 32 MI x 32 NJ each.
+template <int PLANES_, int BM_, int BN_, int MI_, int NJ_, int BK_, int SLOTS_>
+struct Tile {
+  static constexpr int PLANES = PLANES_, BM = BM_, BN = BN_, MI = MI_, NJ = NJ_, BK = BK_, SLOTS = SLOTS_;
+  static constexpr int WN = BN / (32 * NJ), WAVES = BM / (32 * MI) * WN, THREADS = WAVES * 64;
+};
+
+// A problem entry read once from the kernel arguments and kept in scalar
+// registers (see arg_reg).
+__device__ inline GemmProb prob_regs(const GemmProb& p) {
+  GemmProb q;
+  q.a = arg_reg(p.a), q.b = arg_reg(p.b), q.c = arg_reg(p.c), q.o = arg_reg(p.o), q.ot = arg_reg(p.ot);
+  q.a_plane = arg_reg(p.a_plane), q.b_plane = arg_reg(p.b_plane), q.c_plane = arg_reg(p.c_plane);
+  q.o_plane = arg_reg(p.o_plane), q.ot_plane = arg_reg(p.ot_plane);
+  q.a_batch = arg_reg(p.a_batch), q.b_batch = arg_reg(p.b_batch), q.c_batch = arg_reg(p.c_batch);
+  q.o_batch = arg_reg(p.o_batch), q.ot_batch = arg_reg(p.ot_batch);
+  q.lda = arg_reg(p.lda), q.ldb = arg_reg(p.ldb), q.ldo = arg_reg(p.ldo), q.ldot = arg_reg(p.ldot);
+  q.k = arg_reg(p.k), q.tm = arg_reg(p.tm), q.tn = arg_reg(p.tn), q.tiles = arg_reg(p.tiles);
+  q.blk_begin = arg_reg(p.blk_begin), q.unit_begin = arg_reg(p.unit_begin);
+  q.s_acc = arg_reg(p.s_acc), q.s_c = arg_reg(p.s_c), q.d_out = arg_reg(p.d_out), q.d_in = arg_reg(p.d_in);
+  q.d_batch = arg_reg(p.d_batch), q.d_cols = arg_reg(p.d_cols);
+  q.y = arg_reg(p.y), q.w = arg_reg(p.w), q.y_ld = arg_reg(p.y_ld), q.y_batch = arg_reg(p.y_batch);
+  q.rows = arg_reg(p.rows), q.cols = arg_reg(p.cols), q.y_bf16 = arg_reg(p.y_bf16);
+  q.decay = arg_reg(p.decay), q.factor = arg_reg(p.factor);
+  return q;
+}
+
+// Where tile t of a problem lies.
+struct Place {
+  int mat, ti, tj;
+};
+template <bool SYM>
+__device__ inline Place place_of_tile(const GemmProb& P, int t) {
+  Place at;
+  at.mat = t / P.tiles;
+  t -= at.mat * P.tiles;
+  if (SYM) {                       // upper tiles, in bands of kBand rows, column after column
+    int r0 = 0;
+    for (;;) {
+      const int h = min(kBand, P.tn - r0), n = h * (h + 1) / 2 + (P.tn - r0 - h) * h;
+      if (t < n) {
+        int c = 0;
+        while (t >= min(c + 1, h)) t -= min(++c, h);
+        at.ti = r0 + t;
+        at.tj = r0 + c;
+        return at;
+      }
+      t -= n;
+      r0 += h;
+    }
   }
-  const int i0 = ti * BT, j0 = tj * BT;
+  // bands of kBand tile rows, column after column
+  const int band = t / (kBand * P.tn), h = min(kBand, P.tm - band * kBand);
+  t -= band * kBand * P.tn;
+  at.ti = band * kBand + t % h;
+  at.tj = t / h;
+  return at;
+}
+
+template <typename C>
+using Ring = f16[C::SLOTS][C::PLANES][(C::BM + C::BN) * C::BK];
+
+// acc = the product over the stages s0 .. s1 - 1 of a tile.
+template <typename C>
+__device__ inline void sum_stages(const GemmProb& P, const Place& at, int s0, int s1, Ring<C>& ring, f32x16 (&acc)[C::MI][C::NJ]) {
+  constexpr int PLANES = C::PLANES, BM = C::BM, BN = C::BN, MI = C::MI, NJ = C::NJ, BK = C::BK, SLOTS = C::SLOTS;
+  constexpr int THREADS = C::THREADS;
+  constexpr int CHUNKS = BK / 8;                      // 16-byte chunks of a row
+  constexpr int PL = (BM + BN) * BK;                  // elements of a plane of a stage, P's rows first
+  constexpr int LOADS = PL / 8 / THREADS;             // loads a thread and plane
+  constexpr int LOADS_P = BM * BK / 8 / THREADS;      // of these, of P
+  static_assert(BM * BK % (8 * THREADS) == 0 && BN * BK % (8 * THREADS) == 0);
+  const int mat = at.mat, i0 = at.ti * BM, j0 = at.tj * BN;
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-  const int wm = BT == 256 ? (wid >> 2) * 128 : (wid >> 1) * 64;
-  const int wn = BT == 256 ? (wid & 3) * 64 : (wid & 1) * 64;
+  const int wm = wid / C::WN * (32 * MI), wn = wid % C::WN * (32 * NJ);
 
   // operands: a buffer resource of the tile's rows each
   i32x4 rsrc[2][PLANES];
-  uint32_t off[2][LOADS];
+  uint32_t off[LOADS];
+  auto swizzle = [](int row) { return CHUNKS == 8 ? (row >> 1) & 7 : (row >> 2) & 3; };
 #pragma unroll
   for (int op = 0; op < 2; ++op) {
     const int ld = op ? P.ldb : P.lda;
@@ -234,33 +365,30 @@ __global__ void __launch_bounds__(BT == 256 ? 512 : 256) orth_gemm_kernel(GemmBa
 #pragma unroll
     for (int pl = 0; pl < PLANES; ++pl) {
       const uint64_t at = reinterpret_cast<uint64_t>(base + (pl ? (op ? P.b_plane : P.a_plane) : 0));
-      rsrc[op][pl] = i32x4{static_cast<int>(at & 0xffffffffu), static_cast<int>((at >> 32) & 0xffffu), BT * ld * 2, 0x00020000};
+      rsrc[op][pl] = i32x4{__builtin_amdgcn_readfirstlane(static_cast<int>(at & 0xffffffffu)),
+                           __builtin_amdgcn_readfirstlane(static_cast<int>((at >> 32) & 0xffffu)), (op ? BN : BM) * ld * 2, 0x00020000};
     }
+  }
 #pragma unroll
-    for (int u = 0; u < LOADS; ++u) {
-      const int p = u * THREADS + tid, row = p / CHUNKS;
-      const int c = (p % CHUNKS) ^ (CHUNKS == 8 ? (row >> 1) & 7 : (row >> 2) & 3);
-      off[op][u] = static_cast<uint32_t>(row * ld + c * 8) * 2;
-    }
+  for (int u = 0; u < LOADS; ++u) {
+    const int p = u * THREADS + tid, row = p / CHUNKS, r = row < BM ? row : row - BM;
+    off[u] = static_cast<uint32_t>(r * (u < LOADS_P ? P.lda : P.ldb) + ((p % CHUNKS) ^ swizzle(row)) * 8) * 2;
   }
   auto issue = [&](int s, int slot) {
 #pragma unroll
-    for (int op = 0; op < 2; ++op)
+    for (int pl = 0; pl < PLANES; ++pl)
 #pragma unroll
-      for (int pl = 0; pl < PLANES; ++pl)
-#pragma unroll
-        for (int u = 0; u < LOADS; ++u) {
-          const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
-              (__attribute__((address_space(3))) void*)(&ring[slot][op][pl][(u * THREADS + wid * 64) * 8])));
-          asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                       :
-                       : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(static_cast<uint32_t>(s * BK * 2) + off[op][u]),
-                         "s"(rsrc[op][pl])
-                       : "memory", "m0");
-        }
+      for (int u = 0; u < LOADS; ++u) {
+        const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+            (__attribute__((address_space(3))) void*)(&ring[slot][pl][(u * THREADS + wid * 64) * 8])));
+        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :
+                     : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off[u]), "s"(rsrc[u >= LOADS_P][pl]),
+                       "s"(__builtin_amdgcn_readfirstlane(s * BK * 2))
+                     : "memory");
+      }
   };
 
-  f32x16 acc[MI][NJ];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -268,94 +396,337 @@ __global__ void __launch_bounds__(BT == 256 ? 512 : 256) orth_gemm_kernel(GemmBa
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  // a lane's fragment of rows r0 .. r0 + 31 of an operand: row r0 + lane % 32, 8 of the contraction from ks + 8 (lane / 32)
-  auto frag = [&](const f16* op, int r0, int ks) {
+  // a lane's fragment of rows r0 .. r0 + 31: row r0 + lane % 32, 8 of the contraction from ks + 8 (lane / 32)
+  auto frag = [&](const f16* stage, int r0, int ks) {
     const int row = r0 + (lane & 31), c = ks / 8 + (lane >> 5);
-    return *reinterpret_cast<const f16x8*>(op + row * BK + (c ^ (CHUNKS == 8 ? (row >> 1) & 7 : (row >> 2) & 3)) * 8);
+    return *reinterpret_cast<const f16x8*>(stage + row * BK + (c ^ swizzle(row)) * 8);
   };
 
-  const int stages = P.k / BK;
-  issue(0, 0);
-  for (int s = 0; s < stages; ++s) {
-    KFAC_WAIT_VM(0);
+#pragma unroll
+  for (int s = 0; s < SLOTS - 1; ++s) issue(min(s0 + s, s1 - 1), s);       // (a short contraction asks for its last stage again)
+  for (int s = s0, slot = 0; s < s1; ++s, slot = slot + 1 == SLOTS ? 0 : slot + 1) {
+    // this stage has arrived: all but the newest SLOTS - 2 stages' loads
+    KFAC_WAIT_VM((SLOTS - 2) * LOADS * PLANES);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");           // the loads above wrote what is read below
-    if (s + 1 < stages) issue(s + 1, (s + 1) & 1);
-    const int slot = s & 1;
-#pragma unroll
-    for (int ks = 0; ks < BK; ks += 16) {
-      f16x8 fa[PLANES][MI], fb[PLANES][NJ];
+    // into the slot that every wavefront has left; past the end the last stage again, so that counts stay the same
+    issue(min(s + SLOTS - 1, s1 - 1), slot == 0 ? SLOTS - 1 : slot - 1);
+    // the fragments of a step of 16 are read while the products of the one before run
+    f16x8 fa[2][PLANES][MI], fb[2][PLANES][NJ];
+    auto read = [&](int ks, int to) {
 #pragma unroll
       for (int pl = 0; pl < PLANES; ++pl) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i) fa[pl][i] = frag(ring[slot][0][pl], wm + 32 * i, ks);
+        for (int i = 0; i < MI; ++i) fa[to][pl][i] = frag(ring[slot][pl], wm + 32 * i, ks);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) fb[pl][j] = frag(ring[slot][1][pl], wn + 32 * j, ks);
+        for (int j = 0; j < NJ; ++j) fb[to][pl][j] = frag(ring[slot][pl], BM + wn + 32 * j, ks);
       }
+    };
+    constexpr int READS = PLANES * (MI + NJ), MFMAS = (PLANES == 2 ? 3 : 1) * MI * NJ;
+    read(0, 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedDsRead, READS, 0);
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+    for (int ks = 0; ks < BK; ks += 16) {
+      const int cur = (ks / 16) & 1;
+      if (ks + 16 < BK) read(ks + 16, cur ^ 1);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[0][j], acc[i][j], 0, 0, 0);
-          if constexpr (PLANES == 2) {
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[1][j], acc[i][j], 0, 0, 0);
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[1][i], fb[0][j], acc[i][j], 0, 0, 0);
-          }
+      for (int x = 0; x < (PLANES == 2 ? 3 : 1); ++x)      // high x high, high x low, low x high
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[cur][PLANES == 2 && x == 2][i], fb[cur][PLANES == 2 && x == 1][j],
+                                                               acc[i][j], 0, 0, 0);
+      if (ks + 16 < BK) {
+#pragma unroll
+        for (int u = 0; u < READS; ++u) {
+          __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
         }
+        __builtin_amdgcn_sched_group_barrier(kSchedMfma, MFMAS - READS, 0);
+      } else {
+        __builtin_amdgcn_sched_group_barrier(kSchedMfma, MFMAS, 0);
+      }
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);      // lgkmcnt(0): this wavefront has read the slot before the next barrier
   }
 
-  // accumulator r of block (i, j): row 8 (r / 4) + 4 (lane / 32) + r % 4, column lane % 32
-  const bool diag = P.sym && ti == tj;
+  KFAC_WAIT_VM(0);                           // the stages asked for past the end
+  __syncthreads();
+}
+
+// What becomes of a wavefront's sums, 32 rows at a time, through LDS of its own
+// (`mine`): the sums (accumulator r of block (i, j): row 8 (r / 4) + 4 (lane / 32) +
+// r % 4, column lane % 32) are turned into 8 columns a lane, so that C is read and
+// the result written in 16-byte pieces; the result's halves go back to LDS, from
+// where transposing reads give 8 rows a lane for the transpose.  C's next rows are asked
+// for before a row is stored: a load waits for the stores before it.
+constexpr int LS = 68;                       // row length in LDS, of floats and of halves
+constexpr int kMine = 32 * LS;               // floats of a wavefront
+
+template <typename C, Kind KIND>
+__device__ inline void finish(const GemmProb& P, const Place& at, int wid, f32x16 (&acc)[C::MI][C::NJ], float* mine) {
+  constexpr int PLANES = C::PLANES, MI = C::MI, NJ = C::NJ;
+  constexpr bool SYM = KIND == kGram || KIND == kPoly;
+  static_assert(NJ == 2, "64 columns a wavefront");
+  const int mat = at.mat, i0 = at.ti * C::BM, j0 = at.tj * C::BN;
+  const int lane = threadIdx.x & 63;
+  const int wm = wid / C::WN * (32 * MI), wn = wid % C::WN * (32 * NJ);
+  f16* halves = reinterpret_cast<f16*>(mine);
+  const int lr = lane >> 3, lc = (lane & 7) * 8;
+  const int col = j0 + wn + lc;
+  // a symmetric result: 64 x 64 blocks below the diagonal are not written, those on it whole, those above it both ways
+  auto below = [&](int i) { return SYM ? (i0 + wm + 32 * i) / 64 - (j0 + wn) / 64 : -1; };
+  constexpr bool HAS_C = KIND != kGram, C_LOW = PLANES == 2 || KIND >= kNext, LAST = KIND >= kLast;
+  constexpr bool DIAG_IN = PLANES == 1 && KIND >= kNext;
+  const int64_t row_step = static_cast<int64_t>(8) * P.ldo;
+  const f16* c_at = P.c + mat * P.c_batch + static_cast<int64_t>(i0 + wm + lr) * P.ldo + col;
+  f16x8 ch[2][4], cl[2][4];
+  float d_row[2][4] = {};
+  const bool whole = j0 + wn + 64 <= P.cols; // no columns past the matrix (LAST)
+  auto read_c = [&](int i) {
+    if constexpr (!HAS_C) return;
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+    for (int t = 0; t < 4; ++t) {
+      const f16* c = c_at + (4 * i + t) * row_step;
+      ch[i & 1][t] = *reinterpret_cast<const f16x8*>(c);
+      if constexpr (C_LOW) cl[i & 1][t] = *reinterpret_cast<const f16x8*>(c + P.c_plane);
+    }
+    if (DIAG_IN && !P.d_cols) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int col = j0 + wn + 32 * j + (lane & 31);
+      for (int t = 0; t < 4; ++t)
+        d_row[i & 1][t] = P.d_in[static_cast<int64_t>(mat) * P.d_batch + i0 + wm + 32 * i + 8 * t + lr];
+    }
+  };
+  // what multiplies C: s_c, and with it the diagonal that B left out, of the lane's columns or of a row
+  float fc[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row0 = i0 + wm + 32 * i + 8 * q + 4 * (lane >> 5);
+  for (int e = 0; e < 8; ++e) fc[e] = P.s_c;
+  if (DIAG_IN && P.d_cols) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = row0 + e;
-          float v = P.s_acc * acc[i][j][4 * q + e];
-          const int64_t at = static_cast<int64_t>(row) * P.ldo + col;
-          if (P.c) {
-            const f16* c = P.c + mat * P.c_batch + at;
-            float x = static_cast<float>(c[0]);
-            if (PLANES == 2 || P.c_plane) x += static_cast<float>(c[P.c_plane]);
-            if (PLANES == 1 && P.d_in) v = fmaf(P.s_acc * P.d_in[mat * P.d_batch + row], x, v);
-            v = fmaf(P.s_c, x, v);
-          }
-          if constexpr (LAST) {
-            if (row >= P.rows || col >= P.cols) continue;       // rows, cols of X
-            const int64_t to = P.tall ? static_cast<int64_t>(col) * P.y_ld + row : static_cast<int64_t>(row) * P.y_ld + col;
-            if (P.w) {
-              P.w[to] = fmaf(-P.factor, v, P.decay * P.w[to]);
-            } else if (P.y_bf16) {
-              static_cast<unsigned short*>(P.y)[mat * P.y_batch + to] = static_cast<unsigned short>(Elem<__bf16>::bits(v));
-            } else {
-              static_cast<float*>(P.y)[mat * P.y_batch + to] = v;
-            }
+    for (int e = 0; e < 8; ++e) fc[e] = fmaf(P.s_acc, P.d_in[static_cast<int64_t>(mat) * P.d_batch + col + e], P.s_c);
+  }
+  read_c(0);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    if (i + 1 < MI) read_c(i + 1);
+    const int row0 = i0 + wm + 32 * i;
+    if (below(i) > 0) continue;
+    u32x4 keep[8];                           // the result: 4 rows' halves and what they leave
+    u32x4 wv[8];                             // kWeight: the weight's rows
+    if (KIND == kWeight && whole) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float* from = P.w + static_cast<int64_t>(min(row0 + 8 * t + lr, P.rows - 1)) * P.y_ld + col;
+        wv[2 * t] = load16(from);
+        wv[2 * t + 1] = load16(from + 4);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mine[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * LS + 32 * j + (lane & 31)] = acc[i][j][r];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int row = row0 + 8 * t + lr;
+      f32x4* at = reinterpret_cast<f32x4*>(mine + (8 * t + lr) * LS + lc);
+      const f32x4 x0 = at[0], x1 = at[1];
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = P.s_acc * (e < 4 ? x0[e & 3] : x1[e & 3]);
+        if constexpr (HAS_C) {
+          float c = static_cast<float>(ch[i & 1][t][e]);
+          if constexpr (C_LOW) c += static_cast<float>(cl[i & 1][t][e]);
+          v[e] = fmaf(DIAG_IN ? fmaf(P.s_acc, d_row[i & 1][t], fc[e]) : fc[e], c, v[e]);
+        }
+      }
+      if constexpr (LAST) {
+        if (!whole) {
+          at[0] = f32x4{v[0], v[1], v[2], v[3]};
+          at[1] = f32x4{v[4], v[5], v[6], v[7]};
+        } else if (row < P.rows) {
+          const int64_t to = mat * P.y_batch + static_cast<int64_t>(row) * P.y_ld + col;
+          if (KIND == kLast && P.y_bf16) {
+            store16(static_cast<unsigned short*>(P.y) + to, pack16<__bf16>(v));
           } else {
-            if (diag && row > col) continue;
-            if (PLANES == 1 && P.d_out && row == col) {
-              P.d_out[mat * P.d_batch + row] = v;
-              v = 0.f;
+            float* y = (KIND == kWeight ? P.w : static_cast<float*>(P.y)) + to;
+            if constexpr (KIND == kWeight) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = fmaf(-P.factor, v[e], P.decay * __uint_as_float(wv[2 * t + (e >> 2)][e & 3]));
             }
-            f16 hi, lo;
-            split(v, hi, lo);
-            f16* o = P.o + mat * P.o_batch + at;
-            o[0] = hi;
-            if (PLANES == 2 || P.o_plane) o[P.o_plane] = lo;
-            f16* ot = P.ot + mat * P.ot_batch + static_cast<int64_t>(col) * P.ldot + row;
-            ot[0] = hi;
-            if constexpr (PLANES == 2) ot[P.ot_plane] = lo;
+            store16(y, pack16<float>(v));
+            store16(y + 4, pack16<float>(v + 4));
           }
+        }
+      } else {
+        if (KIND == kPoly && PLANES == 1 && below(i) == 0) {
+          float d = 0.f;
+          const int at_e = row - col;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (at_e == e) d = v[e], v[e] = 0.f;
+          if (at_e >= 0 && at_e < 8) P.d_out[static_cast<int64_t>(mat) * P.d_batch + row] = d;
+        }
+        f16x8 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f16 h, l;
+          split(v[e], h, l);
+          hi[e] = h;
+          lo[e] = l;
+        }
+        keep[t] = __builtin_bit_cast(u32x4, hi);
+        if constexpr (PLANES == 2 || KIND == kNext) keep[4 + t] = __builtin_bit_cast(u32x4, lo);
+      }
+    }
+    if constexpr (LAST) {
+      if (!whole && j0 + wn + lane < P.cols) {         // a lane a column
+        const int64_t at = mat * P.y_batch + static_cast<int64_t>(row0) * P.y_ld + j0 + wn + lane;
+#pragma unroll 1
+        for (int r = 0; r < min(32, P.rows - row0); ++r) {
+          const float v = mine[r * LS + lane];
+          const int64_t to = at + r * P.y_ld;
+          if (KIND == kWeight) P.w[to] = fmaf(-P.factor, v, P.decay * P.w[to]);
+          else if (P.y_bf16) Elem<__bf16>::store(P.y, to, v);
+          else static_cast<float*>(P.y)[to] = v;
         }
       }
     }
+    if constexpr (!LAST) {
+      f16* o = P.o + mat * P.o_batch + static_cast<int64_t>(row0 + lr) * P.ldo + col;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        *reinterpret_cast<u32x4*>(o + t * row_step) = keep[t];
+        if constexpr (PLANES == 2 || KIND == kNext) *reinterpret_cast<u32x4*>(o + t * row_step + P.o_plane) = keep[4 + t];
+      }
+      if (below(i) == 0) {
+        __builtin_amdgcn_sched_barrier(0);
+        continue;
+      }
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+      for (int pl = 0; pl < PLANES; ++pl)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          u32x2* to = reinterpret_cast<u32x2*>(halves + pl * 32 * LS + (8 * t + lr) * LS + lc);
+          const u32x4 x = keep[4 * pl + t];
+          to[0] = u32x2{x[0], x[1]};
+          to[1] = u32x2{x[2], x[3]};
+        }
+      // 16 lanes: 4 rows of 16 columns in, a column of 4 rows each out
+      const int g = lane >> 4, s = lane & 15;
+      f16* ot = P.ot + mat * P.ot_batch + static_cast<int64_t>(j0 + wn + s) * P.ldot + row0 + 8 * g;
+#pragma unroll
+      for (int pl = 0; pl < PLANES; ++pl)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f16* from = halves + pl * 32 * LS + (8 * g + (s >> 2)) * LS + 16 * q + 4 * (s & 3);
+          *reinterpret_cast<f16x8*>(ot + static_cast<int64_t>(16 * q) * P.ldot + (pl ? P.ot_plane : 0)) =
+              turned_rows(from, from + 4 * LS);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);       // (rows taken ahead of each other would not fit the registers)
+  }
+}
+
+// The shares of a launch that workgroup w takes, and the first that reaches unit u.
+__device__ inline int64_t share_begin(const GemmBatch& b, int64_t w) { return w * b.units / b.workgroups; }
+__device__ inline int share_of(const GemmBatch& b, int64_t u) {
+  int64_t w = u * b.workgroups / b.units;
+  while (share_begin(b, w + 1) <= u) ++w;
+  while (share_begin(b, w) > u) --w;
+  return static_cast<int>(w);
+}
+
+template <typename C, Kind KIND>
+__global__ void __launch_bounds__(C::THREADS) orth_gemm_kernel(GemmBatch batch) {
+  constexpr bool SYM = KIND == kGram || KIND == kPoly;
+  static_assert(C::BM == C::BN, "symmetric tiles");
+  __shared__ __attribute__((aligned(16))) Ring<C> ring;
+  static_assert(sizeof(ring) >= C::WAVES * kMine * sizeof(float));
+  const int wid = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  float* mine = reinterpret_cast<float*>(&ring[0][0][0]) + wid * kMine;
+  // workgroups go to the 8 XCDs in turn: each XCD takes a run of tiles, so that the
+  // panels that its tiles share are read into its L2 once
+  const int per = gridDim.x / 8, w0 = blockIdx.x;
+  const int w = w0 < 8 * per ? (w0 % 8) * per + w0 / 8 : w0;
+  f32x16 acc[C::MI][C::NJ];
+  if (batch.units == 0) {
+    int pi = 0;
+    while (pi + 1 < batch.n && batch.p[pi + 1].blk_begin <= w) ++pi;
+    const GemmProb P = prob_regs(batch.p[pi]);
+    const Place at = place_of_tile<SYM>(P, w - P.blk_begin);
+    sum_stages<C>(P, at, 0, P.k / C::BK, ring, acc);
+    finish<C, KIND>(P, at, wid, acc, mine);
+    return;
+  }
+  const int64_t end = share_begin(batch, w + 1);
+  bool first = true;
+  for (int64_t u = share_begin(batch, w); u < end; first = false) {
+    int pi = 0;
+    while (pi + 1 < batch.n && batch.p[pi + 1].unit_begin <= u) ++pi;
+    const GemmProb P = prob_regs(batch.p[pi]);
+    const int stages = P.k / C::BK;
+    const int64_t in = u - P.unit_begin;
+    const int tile = static_cast<int>(in / stages), s0 = static_cast<int>(in - static_cast<int64_t>(tile) * stages);
+    const int s1 = static_cast<int>(min(static_cast<int64_t>(stages), s0 + end - u));
+    const Place at = place_of_tile<SYM>(P, tile);
+    sum_stages<C>(P, at, s0, s1, ring, acc);
+    if (s0 == 0 && s1 == stages) {
+      finish<C, KIND>(P, at, wid, acc, mine);
+      __syncthreads();                       // the ring is the next tile's
+    } else {
+      f32x4* to = reinterpret_cast<f32x4*>(batch.partial + (2 * static_cast<int64_t>(w) + !first) * (C::BM * C::BN)) +
+                  wid * (C::MI * C::NJ * 4 * 64) + lane;
+#pragma unroll
+      for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+        for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            to[((i * C::NJ + j) * 4 + q) * 64] = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    }
+    u += s1 - s0;
+  }
+}
+
+// A wavefront's part of a tile whose stages were shared: the shares in order.
+template <typename C, Kind KIND>
+__global__ void __launch_bounds__(64) orth_join_kernel(GemmBatch batch) {
+  constexpr bool SYM = KIND == kGram || KIND == kPoly;
+  __shared__ __attribute__((aligned(16))) float mine[kMine];
+  const int lane = threadIdx.x, wid = blockIdx.x % C::WAVES, tile = blockIdx.x / C::WAVES;
+  int pi = 0;
+  while (pi + 1 < batch.n && batch.p[pi + 1].blk_begin <= tile) ++pi;
+  const GemmProb P = prob_regs(batch.p[pi]);
+  const int stages = P.k / C::BK;
+  const int64_t begin = P.unit_begin + static_cast<int64_t>(tile - P.blk_begin) * stages;
+  const int w0 = share_of(batch, begin), w1 = share_of(batch, begin + stages - 1);
+  if (w0 == w1) return;                      // one workgroup had all of it
+  f32x16 acc[C::MI][C::NJ];
+#pragma unroll
+  for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  for (int w = w0; w <= w1; ++w) {
+    const int second = w == w0 && share_begin(batch, w) < begin;
+    const f32x4* from = reinterpret_cast<const f32x4*>(batch.partial + (2 * static_cast<int64_t>(w) + second) * (C::BM * C::BN)) +
+                        wid * (C::MI * C::NJ * 4 * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 x = from[((i * C::NJ + j) * 4 + q) * 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += x[e];
+        }
+  }
+  finish<C, KIND>(P, place_of_tile<SYM>(P, tile - P.blk_begin), wid, acc, mine);
 }
 
 // -- plan ----------------------------------------------------------------------
@@ -372,7 +743,8 @@ Shape shape_of(const OrthTask& t) {
   s.d = std::min(t.rows, t.cols);
   s.n = std::max(t.rows, t.cols);
   s.tall = t.rows > t.cols;
-  s.tile = s.d >= 2048 ? 256 : 128;
+  // whole tiles of 256 where that adds less than an eighth to a side
+  s.tile = round_up(s.d, 256) * 8 <= round_up(s.d, 128) * 9 && round_up(s.n, 256) * 8 <= round_up(s.n, 128) * 9 ? 256 : 128;
   s.dp = round_up(s.d, s.tile);
   s.np = round_up(s.n, s.tile);
   s.x_plane = static_cast<int64_t>(s.dp) * s.np;
@@ -381,7 +753,7 @@ Shape shape_of(const OrthTask& t) {
 }
 
 struct Region {
-  size_t part, x, xt[2], a, b, diag;
+  size_t part, same[2], turned[2], a, b, diag;      // X as x lies and turned; what B X reads is not what it writes
 };
 size_t plan(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how, std::vector<Region>* out) {
   const int planes = how.products == KFAC_PRODUCTS_FULL ? 2 : 1;
@@ -396,9 +768,11 @@ size_t plan(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how, st
     Region r;
     const size_t batch = static_cast<size_t>(t.batch);
     r.part = take(sizeof(double) * kNormBlocks * batch);
-    r.x = take(2 * 2 * batch * s.x_plane);
-    r.xt[0] = take(2 * planes * batch * s.x_plane);
-    r.xt[1] = take(2 * planes * batch * s.x_plane);
+    const size_t both = 2 * 2 * batch * s.x_plane, some = 2 * planes * batch * s.x_plane;
+    r.same[0] = take(both);
+    r.same[1] = s.tall ? take(both) : r.same[0];
+    r.turned[0] = take(some);
+    r.turned[1] = s.tall ? r.turned[0] : take(some);
     r.a = take(2 * planes * batch * s.a_plane);
     r.b = take(2 * planes * batch * s.a_plane);
     r.diag = take(sizeof(float) * batch * s.dp);
@@ -426,50 +800,133 @@ std::vector<StepScale> step_scales(const kfac_orthogonal_t& how, int* last) {
   return out;
 }
 
-template <bool LAST>
-kfac_status_t launch_products(const std::vector<GemmProb>& probs, const std::vector<int>& tile, const std::vector<int>& batch,
-                              int planes, hipStream_t st) {
-  for (int bt : {256, 128}) {
-    size_t i = 0;
-    while (i < probs.size()) {
-      GemmBatch b{};
-      int64_t blocks = 0;
-      for (; i < probs.size() && b.n < kMaxProbs; ++i) {
-        if (tile[i] != bt) continue;
-        GemmProb p = probs[i];
-        if (blocks + static_cast<int64_t>(p.tiles) * batch[i] > (1 << 22)) {
-          if (b.n) break;                 // the rest in a launch of their own
-        }
-        p.blk_begin = static_cast<int>(blocks);
-        blocks += static_cast<int64_t>(p.tiles) * batch[i];
-        b.p[b.n++] = p;
-      }
-      if (b.n == 0) continue;
-      const dim3 grid(static_cast<uint32_t>(blocks)), block(bt == 256 ? 512 : 256);
-      if (planes == 2) {
-        if (bt == 256) hipLaunchKernelGGL((orth_gemm_kernel<2, 256, LAST>), grid, block, 0, st, b);
-        else hipLaunchKernelGGL((orth_gemm_kernel<2, 128, LAST>), grid, block, 0, st, b);
-      } else {
-        if (bt == 256) hipLaunchKernelGGL((orth_gemm_kernel<1, 256, LAST>), grid, block, 0, st, b);
-        else hipLaunchKernelGGL((orth_gemm_kernel<1, 128, LAST>), grid, block, 0, st, b);
-      }
-      if (hipGetLastError() != hipSuccess) return KFAC_ERR_HIP;
+using Half256 = Tile<1, 256, 256, 4, 2, 64, 2>;
+using Half128 = Tile<1, 128, 128, 2, 2, 64, 2>;
+using Full256 = Tile<2, 256, 256, 4, 2, 32, 2>;
+using Full128 = Tile<2, 128, 128, 2, 2, 32, 2>;
+
+// How a launch's tiles are cut: their size, and the workgroups that share their
+// stages (0: each takes a tile).
+struct Cut {
+  int tile, shares;
+};
+struct Product {
+  int64_t tiles[2], units[2];      // of 128 and of 256
+};
+// The cut that takes least time, by what the kernels measured: a stage of one
+// workgroup a compute unit (two, for tiles of 128, where there are that many), an
+// epilogue, and shares written and read again at 4 TB/s with a launch of their own.
+Cut cut_of(const Product& p, int planes, bool may256) {
+  Cut best{128, 0};
+  double least = 1e30;
+  for (int big = may256 ? 1 : 0; big >= 0; --big) {
+    const double tiles = static_cast<double>(p.tiles[big]), units = static_cast<double>(p.units[big]), stages = units / tiles;
+    const int slots = big ? 256 : 512;
+    auto stage = [&](double running) {
+      if (big) return planes == 2 ? 2.1 : 1.4;
+      return running > 256 ? (planes == 2 ? 1.45 : 0.8) : (planes == 2 ? 1.0 : 0.55);
+    };
+    const double rounds = std::ceil(tiles / slots), end = big ? 30.0 : 12.0;
+    const double whole = rounds * (stages * stage(std::min(tiles, static_cast<double>(slots))) + end);
+    if (whole < least) least = whole, best = {big ? 256 : 128, 0};
+    const double bytes = big ? 524288.0 : 131072.0;          // a share's sums, written and read
+    for (int g = 32; g <= slots; g += 32) {
+      if (units < 2.0 * g || g < tiles * 0.5) continue;
+      // (workgroups at different places of the contraction read no panels together)
+      const double t = units / g * stage(0) * (1.0 + g / (big ? 256.0 : 350.0)) + (g + tiles) * bytes / 4e6 + 10.0 + end;
+      if (t < 0.95 * least) least = t, best = {big ? 256 : 128, g};
     }
   }
-  return KFAC_OK;
+  return best;
 }
+
+template <typename C, Kind KIND>
+kfac_status_t launch_tiles(std::vector<GemmProb>& probs, const std::vector<int>& batch, int shares, float* partial, hipStream_t st) {
+  GemmBatch b{};
+  int64_t tiles = 0, units = 0;
+  for (size_t i = 0; i < probs.size(); ++i) {
+    GemmProb& p = probs[i];
+    p.tm /= C::BM;                  // rows and columns so far
+    p.tn /= C::BN;
+    p.tiles = KIND == kGram || KIND == kPoly ? p.tn * (p.tn + 1) / 2 : p.tm * p.tn;
+    p.blk_begin = static_cast<int>(tiles);
+    p.unit_begin = units;
+    tiles += static_cast<int64_t>(p.tiles) * batch[i];
+    units += static_cast<int64_t>(p.tiles) * batch[i] * (p.k / C::BK);
+    b.p[b.n++] = p;
+  }
+  b.workgroups = shares;
+  b.units = shares ? units : 0;
+  b.partial = partial;
+  hipLaunchKernelGGL((orth_gemm_kernel<C, KIND>), dim3(static_cast<uint32_t>(shares ? shares : tiles)), dim3(C::THREADS), 0, st, b);
+  if (shares)
+    hipLaunchKernelGGL((orth_join_kernel<C, KIND>), dim3(static_cast<uint32_t>(tiles * C::WAVES)), dim3(64), 0, st, b);
+  return hipGetLastError() == hipSuccess ? KFAC_OK : KFAC_ERR_HIP;
+}
+
+template <Kind KIND>
+kfac_status_t launch_products(std::vector<GemmProb>& probs, const std::vector<int>& batch, int planes, Cut cut, float* partial, hipStream_t st) {
+  if (planes == 2)
+    return cut.tile == 256 ? launch_tiles<Full256, KIND>(probs, batch, cut.shares, partial, st)
+                           : launch_tiles<Full128, KIND>(probs, batch, cut.shares, partial, st);
+  return cut.tile == 256 ? launch_tiles<Half256, KIND>(probs, batch, cut.shares, partial, st)
+                         : launch_tiles<Half128, KIND>(probs, batch, cut.shares, partial, st);
+}
+
+// Matrices whose products go into the same launches.
+struct Group {
+  std::vector<size_t> tasks;
+  Cut gram, poly, next;
+};
+std::vector<Group> groups_of(const std::vector<OrthTask>& tasks, int planes) {
+  std::vector<Group> out;
+  for (int tile : {256, 128}) {
+    Group g;
+    auto close = [&] {
+      if (g.tasks.empty()) return;
+      Product a{}, b{}, x{};
+      for (size_t i : g.tasks) {
+        const Shape s = shape_of(tasks[i]);
+        for (int big = 0; big < 2; ++big) {
+          const int bt = big ? 256 : 128, bk = planes == 2 ? 32 : 64;
+          const int64_t nd = s.dp / bt, nn = s.np / bt, batch = tasks[i].batch;
+          const int64_t upper = nd * (nd + 1) / 2 * batch, all = nd * nn * batch;
+          a.tiles[big] += upper, a.units[big] += upper * (s.np / bk);
+          b.tiles[big] += upper, b.units[big] += upper * (s.dp / bk);
+          x.tiles[big] += all, x.units[big] += all * (s.dp / bk);
+        }
+      }
+      g.gram = cut_of(a, planes, tile == 256);
+      g.poly = cut_of(b, planes, tile == 256);
+      g.next = cut_of(x, planes, tile == 256);
+      out.push_back(g);
+      g = Group{};
+    };
+    for (size_t i = 0; i < tasks.size(); ++i) {
+      if (shape_of(tasks[i]).tile != tile) continue;
+      g.tasks.push_back(i);
+      if (g.tasks.size() == kMaxProbs) close();
+    }
+    close();
+  }
+  return out;
+}
+size_t partial_bytes(const Cut& c) { return static_cast<size_t>(c.shares) * 2 * c.tile * c.tile * sizeof(float); }
 
 }  // namespace
 
 size_t orth_workspace_bytes(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how) {
-  return plan(tasks, how, nullptr);
+  size_t partial = 0;
+  for (const Group& g : groups_of(tasks, how.products == KFAC_PRODUCTS_FULL ? 2 : 1))
+    for (const Cut& c : {g.gram, g.poly, g.next}) partial = std::max(partial, partial_bytes(c));
+  return plan(tasks, how, nullptr) + partial;
 }
 
 kfac_status_t launch_orthogonal(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how, const OrthStep& step,
                                 char* ws, hipStream_t st) {
   const int planes = how.products == KFAC_PRODUCTS_FULL ? 2 : 1;
   std::vector<Region> regions;
-  plan(tasks, how, &regions);
+  float* partial = reinterpret_cast<float*>(ws + plan(tasks, how, &regions));
   int last_bits = 0;
   const std::vector<StepScale> scales = step_scales(how, &last_bits);
 
@@ -496,21 +953,18 @@ kfac_status_t launch_orthogonal(const std::vector<OrthTask>& tasks, const kfac_o
       p.cols = t.cols;
       p.batch = t.batch;
       p.bf16 = t.dtype == KFAC_BF16;
-      p.blocks = std::min(t.rows, kNormBlocks);
+      p.blocks = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(t.rows) * ((t.cols + 7) / 8) + 1023) / 1024, kNormBlocks));
       p.blk_begin = static_cast<int>(blocks);
       blocks += static_cast<int64_t>(p.blocks) * t.batch;
       p.part = reinterpret_cast<double*>(ws + r.part);
       p.bias = t.bias;
       p.bias_mom = t.bias_mom;
       p.bias_grad = t.bias_grad;
-      f16* x = reinterpret_cast<f16*>(ws + r.x);
-      f16* xt = reinterpret_cast<f16*>(ws + r.xt[0]);
-      p.same = s.tall ? xt : x;
-      p.turned = s.tall ? x : xt;
+      p.same = reinterpret_cast<f16*>(ws + r.same[0]);
+      p.turned = reinterpret_cast<f16*>(ws + r.turned[0]);
       p.plane = s.x_plane;
-      p.same_stride = s.x_plane * (s.tall ? planes : 2);
-      p.turned_stride = s.x_plane * (s.tall ? 2 : planes);
-      p.tall = s.tall;
+      p.same_stride = s.x_plane * 2;
+      p.turned_stride = s.x_plane * planes;
       p.rows_p = s.tall ? s.np : s.dp;
       p.cols_p = s.tall ? s.dp : s.np;
       p.tiles_c = p.cols_p / 64;
@@ -525,41 +979,37 @@ kfac_status_t launch_orthogonal(const std::vector<OrthTask>& tasks, const kfac_o
     if (hipGetLastError() != hipSuccess) return KFAC_ERR_HIP;
   }
 
-  std::vector<int> tile, batch;
-  for (const OrthTask& t : tasks) {
-    tile.push_back(shape_of(t).tile);
-    batch.push_back(t.batch);
-  }
   auto two = [](int e) { return std::ldexp(1.f, e); };
+  for (const Group& g : groups_of(tasks, planes))
   for (int k = 0; k < how.steps; ++k) {
     const float a = how.coefs[3 * k], b = how.coefs[3 * k + 1], c = how.coefs[3 * k + 2];
     const StepScale& sc = scales[k];
     const bool last = k + 1 == how.steps;
     const int xb = last ? 0 : scales[k + 1].x;         // the last X is written as it is
     std::vector<GemmProb> pa, pb, px;
-    for (size_t i = 0; i < tasks.size(); ++i) {
+    std::vector<int> batch;
+    for (size_t i : g.tasks) {
       const OrthTask& t = tasks[i];
+      batch.push_back(t.batch);
       const Shape s = shape_of(t);
       const Region& r = regions[i];
-      f16* x = reinterpret_cast<f16*>(ws + r.x);
-      f16* xt = reinterpret_cast<f16*>(ws + r.xt[k & 1]);
-      f16* xt_next = reinterpret_cast<f16*>(ws + r.xt[(k + 1) & 1]);
+      // X as x lies, [rows_p, cols_p], and turned; the one with d rows and n columns
+      f16* same = reinterpret_cast<f16*>(ws + r.same[k & 1]);
+      f16* turned = reinterpret_cast<f16*>(ws + r.turned[k & 1]);
       f16* A = reinterpret_cast<f16*>(ws + r.a);
       f16* B = reinterpret_cast<f16*>(ws + r.b);
-      const int nd = s.dp / s.tile;
+      const int64_t a_plane2 = planes == 2 ? s.a_plane : 0;
       GemmProb p{};
-      p.a = p.b = x;
+      p.a = p.b = s.tall ? turned : same;
       p.a_plane = p.b_plane = s.x_plane;
-      p.a_batch = p.b_batch = s.x_plane * 2;
+      p.a_batch = p.b_batch = s.x_plane * (s.tall ? planes : 2);
       p.lda = p.ldb = s.np;
       p.o = p.ot = A;
-      p.o_plane = p.ot_plane = planes == 2 ? s.a_plane : 0;
+      p.o_plane = p.ot_plane = a_plane2;
       p.o_batch = p.ot_batch = s.a_plane * planes;
       p.ldo = p.ldot = s.dp;
       p.k = s.np;
-      p.tn = nd;
-      p.tiles = nd * (nd + 1) / 2;
-      p.sym = 1;
+      p.tm = p.tn = s.dp;
       p.s_acc = two(sc.a - 2 * sc.x);
       pa.push_back(p);
       p.a = p.b = A;
@@ -567,7 +1017,7 @@ kfac_status_t launch_orthogonal(const std::vector<OrthTask>& tasks, const kfac_o
       p.a_batch = p.b_batch = s.a_plane * planes;
       p.lda = p.ldb = s.dp;
       p.c = A;
-      p.c_plane = planes == 2 ? s.a_plane : 0;
+      p.c_plane = a_plane2;
       p.c_batch = s.a_plane * planes;
       p.o = p.ot = B;
       p.d_out = reinterpret_cast<float*>(ws + r.diag);
@@ -576,43 +1026,48 @@ kfac_status_t launch_orthogonal(const std::vector<OrthTask>& tasks, const kfac_o
       p.s_acc = c * two(sc.b - 2 * sc.a);
       p.s_c = b * two(sc.b - sc.a);
       pb.push_back(p);
-      p.a = B;
+      // B X, or X^T B where x is taller than wide
+      const f16* xt = s.tall ? same : turned;
+      const int64_t xt_batch = s.x_plane * (s.tall ? 2 : planes);
+      p.a = s.tall ? xt : B;
+      p.b = s.tall ? B : xt;
+      p.a_plane = s.tall ? s.x_plane : s.a_plane;
+      p.b_plane = s.tall ? s.a_plane : s.x_plane;
+      p.a_batch = s.tall ? xt_batch : s.a_plane * planes;
+      p.b_batch = s.tall ? s.a_plane * planes : xt_batch;
       p.d_in = p.d_out;
+      p.d_cols = s.tall;
       p.d_out = nullptr;
-      p.b = xt;
-      p.b_plane = s.x_plane;
-      p.b_batch = s.x_plane * planes;
-      p.c = x;
-      p.c_plane = s.x_plane;
-      p.c_batch = s.x_plane * 2;
-      p.o = x;
-      p.o_plane = s.x_plane;
-      p.o_batch = s.x_plane * 2;
-      p.ldo = s.np;
-      p.ot = xt_next;
+      p.c = same;
+      p.o = reinterpret_cast<f16*>(ws + r.same[(k + 1) & 1]);
+      p.c_plane = p.o_plane = s.x_plane;
+      p.c_batch = p.o_batch = s.x_plane * 2;
+      p.ldo = s.tall ? s.dp : s.np;
+      p.ot = reinterpret_cast<f16*>(ws + r.turned[(k + 1) & 1]);
       p.ot_plane = s.x_plane;
       p.ot_batch = s.x_plane * planes;
-      p.ldot = s.dp;
-      p.tn = s.np / s.tile;
-      p.tiles = nd * p.tn;
-      p.sym = 0;
+      p.ldot = s.tall ? s.np : s.dp;
+      p.tm = s.tall ? s.np : s.dp;
+      p.tn = s.tall ? s.dp : s.np;
       p.s_acc = two(xb - sc.b - sc.x);
       p.s_c = a * two(xb - sc.x);
       p.y = t.y;
       p.w = t.w;
       p.y_ld = t.w ? t.cols : t.y_ld;
-      p.y_batch = t.y_stride;
-      p.rows = s.d;
-      p.cols = s.n;
-      p.tall = s.tall;
+      p.y_batch = t.w ? 0 : t.y_stride;
+      p.rows = t.rows;
+      p.cols = t.cols;
       p.y_bf16 = t.dtype == KFAC_BF16;
       p.decay = 1.f - step.lr * step.weight_decay;
       p.factor = t.factor;
       px.push_back(p);
     }
-    kfac_status_t r = launch_products<false>(pa, tile, batch, planes, st);
-    if (r == KFAC_OK) r = launch_products<false>(pb, tile, batch, planes, st);
-    if (r == KFAC_OK) r = last ? launch_products<true>(px, tile, batch, planes, st) : launch_products<false>(px, tile, batch, planes, st);
+    kfac_status_t r = launch_products<kGram>(pa, batch, planes, g.gram, partial, st);
+    if (r == KFAC_OK) r = launch_products<kPoly>(pb, batch, planes, g.poly, partial, st);
+    if (r == KFAC_OK)
+      r = !last ? launch_products<kNext>(px, batch, planes, g.next, partial, st)
+          : px[0].w ? launch_products<kWeight>(px, batch, planes, g.next, partial, st)
+                    : launch_products<kLast>(px, batch, planes, g.next, partial, st);
     if (r != KFAC_OK) return r;
   }
   return KFAC_OK;
