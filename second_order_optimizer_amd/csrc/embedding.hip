@@ -6,13 +6,16 @@
 // The gradient adds a token's rows in the order of their positions, so that it
 // does not depend on scheduling: positions are sorted by token with a stable
 // radix sort (tiles of positions, a histogram and a scatter a pass), a token's
-// rows are then a run of the sorted positions.  Wavefronts walk the tokens, 64
-// of them each; a token with more than kLong rows is left to the tiles of kLong
-// sorted positions, whose partial sums are joined in order, so that a token that
-// fills a tenth of the batch does not wait for one wavefront.
+// rows are then a run of the sorted positions.  These are cut into tiles of equal
+// length, whatever the tokens: a wavefront adds a tile's rows one after the other
+// and writes each token's sum as its run ends.  A run that crosses a tile's border
+// leaves a part in each tile, and the tile in which it begins has them joined, in
+// order.  So a token that fills a tenth of the batch is many wavefronts' work, and
+// one of which the batch has a single row no wavefront's of its own.
 #include "tokens.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace kfac {
 
@@ -23,7 +26,10 @@ constexpr int kSortWaves = 8, kSortThreads = kSortWaves * kWave;
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kMostTiles = 256;           // tiles of a sort: every workgroup of a scatter reads all their histograms
 constexpr int kLeastTile = 1024;
-constexpr int kLong = 128;
+constexpr int kAhead = 8;                 // rows asked for before they are added
+constexpr int kTile = 32;                 // sorted positions of a tile: fewer where there are few, so that
+constexpr int kSumTiles = 1024;           // enough workgroups run, more where there are many, so that few
+constexpr int kMostSumTiles = 4096;       // parts are joined
 
 struct SortPlan {
   int64_t tile;       // positions a workgroup sorts, a multiple of kSortThreads
@@ -39,6 +45,15 @@ SortPlan sort_plan(int64_t tokens, int32_t vocab) {
   p.passes = (bits + kDigitBits - 1) / kDigitBits;
   p.bits = (bits + p.passes - 1) / p.passes;
   return p;
+}
+
+// Floats of a part: a row's columns, in whole vectors of a lane.
+size_t part_ld(int32_t width) { return align_up(static_cast<size_t>(width), 8); }
+
+// Sorted positions of a tile of the sums.
+int sum_tile(int64_t tokens) {
+  auto share = [&](int tiles, int of) { return ((tokens + tiles - 1) / tiles + of - 1) / of * of; };
+  return static_cast<int>(std::max(std::min<int64_t>(kTile, std::max<int64_t>(kAhead, share(kSumTiles, kAhead))), share(kMostSumTiles, kTile) <= kTile ? 0 : share(kMostSumTiles, kTile)));
 }
 
 struct Regions {
@@ -58,7 +73,8 @@ Regions regions(int64_t tokens, int32_t vocab, int32_t width) {
     r.perm[i] = take(4 * static_cast<size_t>(tokens));
   }
   r.hist = take(4 * static_cast<size_t>(p.tiles) * kDigits);
-  r.partial = take(8 * static_cast<size_t>(width) * static_cast<size_t>((tokens + kLong - 1) / kLong));
+  const int64_t tile = sum_tile(tokens);
+  r.partial = take(8 * part_ld(width) * static_cast<size_t>((tokens + tile - 1) / tile));
   r.bytes = at;
   return r;
 }
@@ -66,14 +82,14 @@ Regions regions(int64_t tokens, int32_t vocab, int32_t width) {
 // -- vectors ----------------------------------------------------------------
 
 // N values of a row from column c on, of `width` columns; those past it read as 0.
-template <typename T, int N>
+template <typename T, int N, bool NT = false>
 __device__ inline void load_cols(float (&f)[N], const char* row, int c, int width) {
   constexpr int VE = Elem<T>::VE;
   if (c + N <= width) {
     if constexpr (N >= VE) {
 #pragma unroll
       for (int q = 0; q < N / VE; ++q) {
-        const u32x4 v = load16(row + static_cast<int64_t>(c + q * VE) * sizeof(T));
+        const u32x4 v = load16<NT>(row + static_cast<int64_t>(c + q * VE) * sizeof(T));
 #pragma unroll
         for (int i = 0; i < VE; ++i) f[q * VE + i] = Elem<T>::get(v, i);
       }
@@ -89,13 +105,13 @@ __device__ inline void load_cols(float (&f)[N], const char* row, int c, int widt
     for (int i = 0; i < N; ++i) f[i] = c + i < width ? Elem<T>::load(row, c + i) : 0.f;
   }
 }
-template <typename T, int N>
+template <typename T, int N, bool NT = false>
 __device__ inline void store_cols(char* row, int c, int width, const float (&f)[N]) {
   constexpr int VE = Elem<T>::VE;
   if (c + N <= width) {
     if constexpr (N >= VE) {
 #pragma unroll
-      for (int q = 0; q < N / VE; ++q) store16(row + static_cast<int64_t>(c + q * VE) * sizeof(T), pack16<T>(f + q * VE));
+      for (int q = 0; q < N / VE; ++q) store16<NT>(row + static_cast<int64_t>(c + q * VE) * sizeof(T), pack16<T>(f + q * VE));
     } else {
       float g[VE];
 #pragma unroll
@@ -110,9 +126,11 @@ __device__ inline void store_cols(char* row, int c, int width, const float (&f)[
       if (c + i < width) Elem<T>::store(row, c + i, f[i]);
   }
 }
-// Columns a lane takes at a time: 16 bytes of the rows of dtype.
-template <typename TY>
-constexpr int kCols = Elem<TY>::VE;
+// Columns a lane takes at a time: 16 bytes of the wider type, so that the lanes of
+// a store lie side by side (two stores of 16 bytes a lane, 32 bytes apart between
+// lanes, past the cache: 65536 x 4096 f32 422 instead of ... us).
+template <typename TT, typename TY>
+constexpr int kCols = Elem<TT>::VE < Elem<TY>::VE ? Elem<TT>::VE : Elem<TY>::VE;
 
 // -- lookup -----------------------------------------------------------------
 
@@ -126,9 +144,9 @@ struct LookupArgs {
   uint32_t* flags;
 };
 
-template <typename TT, typename TY, int TEAM>
+template <typename TT, typename TY, int TEAM, bool NT>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(LookupArgs a) {
-  constexpr int N = kCols<TY>, TEAMS = kThreads / TEAM;
+  constexpr int N = Elem<TY>::VE, TEAMS = kThreads / TEAM;
   const int lane = threadIdx.x % TEAM;
   const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM; t < a.tokens; t += step) {
@@ -147,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(LookupArgs a) {
 #pragma unroll
         for (int i = 0; i < N; ++i) f[i] = 0.f;
       }
-      store_cols<TY, N>(to, c, a.width, f);
+      store_cols<TY, N, NT>(to, c, a.width, f);
     }
   }
 }
@@ -199,9 +217,10 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(SortArgs a) {
   for (int w = 0; w < kSortWaves; ++w) base[w][tid] = 0;
   // this digit in earlier tiles, and in all
   uint32_t before = 0, total = 0;
+#pragma unroll 8
   for (int b = 0; b < a.tiles; ++b) {
     const uint32_t n = a.hist[static_cast<int64_t>(b) * kDigits + tid];
-    if (b < static_cast<int>(blockIdx.x)) before += n;
+    before += b < static_cast<int>(blockIdx.x) ? n : 0;
     total += n;
   }
   const uint32_t upto = wave_scan(total);
@@ -243,6 +262,78 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(SortArgs a) {
   }
 }
 
+// The whole sort of up to kSmall positions in one workgroup, in LDS.
+constexpr int kSmall = 8192;
+constexpr int kSmallWaves = 16, kSmallThreads = kSmallWaves * kWave;
+
+__global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(SortArgs a, int passes) {
+  __shared__ uint32_t keys[2][kSmall];
+  __shared__ uint16_t perm[2][kSmall];
+  __shared__ uint32_t base[kSmallWaves][kDigits];
+  __shared__ uint32_t wave_total[kDigits / kWave];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int n = static_cast<int>(a.tokens);
+  const uint32_t mask = (1u << a.bits) - 1;
+  for (int t = tid; t < n; t += kSmallThreads) {
+    if (load_index(a.ids, t, a.id_type) >= a.vocab) raise_flag(a.flags, KFAC_FLAG_BAD_INDEX);
+    keys[0][t] = key_at<true>(a, t);
+    perm[0][t] = static_cast<uint16_t>(t);
+  }
+  const int run = ((n + kSmallWaves - 1) / kSmallWaves + kWave - 1) / kWave * kWave;
+  const int r0 = wave * run, r1 = min(r0 + run, n);
+  for (int pass = 0; pass < passes; ++pass) {
+    const int from = pass & 1, shift = pass * a.bits;
+    for (int i = tid; i < kSmallWaves * kDigits; i += kSmallThreads) base[i / kDigits][i % kDigits] = 0;
+    __syncthreads();
+    for (int t = r0 + lane; t < r1; t += kWave) atomicAdd(&base[wave][(keys[from][t] >> shift) & mask], 1u);
+    __syncthreads();
+    uint32_t total = 0, upto = 0;
+    if (tid < kDigits) {
+      for (int w = 0; w < kSmallWaves; ++w) total += base[w][tid];
+      upto = wave_scan(total);
+      if (lane == kWave - 1) wave_total[wave] = upto;
+    }
+    __syncthreads();
+    if (tid < kDigits) {
+      uint32_t place = upto - total;
+      for (int w = 0; w < wave; ++w) place += wave_total[w];
+      for (int w = 0; w < kSmallWaves; ++w) {
+        const uint32_t c = base[w][tid];
+        base[w][tid] = place;
+        place += c;
+      }
+    }
+    __syncthreads();
+    for (int t = r0; t < r1; t += kWave) {
+      const bool in = t + lane < r1;
+      const uint32_t key = in ? keys[from][t + lane] : 0;
+      const uint32_t digit = (key >> shift) & mask;
+      uint64_t same = __ballot(in);
+      for (int b = 0; b < a.bits; ++b) {
+        const uint64_t set = __ballot((digit >> b) & 1);
+        same &= (digit >> b) & 1 ? set : ~set;
+      }
+      const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+      uint32_t to = 0;
+      if (in) to = base[wave][digit] + rank;
+      __builtin_amdgcn_wave_barrier();
+      if (in && rank == 0) base[wave][digit] = to + __popcll(same);
+      __builtin_amdgcn_wave_barrier();
+      if (in) {
+        const uint32_t position = perm[from][t + lane];
+        if (pass + 1 == passes) {
+          a.keys_out[to] = key;
+          a.perm_out[to] = position;
+        } else {
+          keys[from ^ 1][to] = key;
+          perm[from ^ 1][to] = static_cast<uint16_t>(position);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // -- sums -------------------------------------------------------------------
 
 struct SumArgs {
@@ -250,9 +341,10 @@ struct SumArgs {
   char* grad;
   int32_t* counts;
   const uint32_t *keys, *perm;
-  float* partial;                      // [tiles of kLong sorted positions][2][width]
-  int64_t tokens, dy_ld, grad_ld;      // strides in bytes
-  int32_t vocab, width, accumulate;
+  float* partial;                      // [tiles][2][part_ld]
+  int64_t tokens, dy_ld, grad_ld, part_ld;      // strides of dy and grad in bytes
+  int32_t vocab, width, accumulate, tile;
+  int32_t tiles, fill_first;           // the first group of tokens that the join's launch fills
   float scale;
 };
 
@@ -267,110 +359,125 @@ __device__ inline int64_t first_at(const uint32_t* keys, int64_t n, uint32_t v) 
   return lo;
 }
 
-template <typename TY, int N>
-__device__ inline void add_row(float (&s)[N], const char* row, int c, int width) {
-  float f[N];
-  load_cols<TY, N>(f, row, c, width);
-#pragma unroll
-  for (int i = 0; i < N; ++i) s[i] += f[i];
-}
-template <typename TT, int N>
-__device__ inline void write_sum(const SumArgs& a, int64_t v, int c, float (&s)[N]) {
+template <typename TT, int N, bool NT>
+__device__ inline void write_sum(const SumArgs& a, int64_t v, int c, const float (&s)[N]) {
   char* row = a.grad + v * a.grad_ld;
+  float f[N];
   if (a.accumulate) {
-    float old[N];
-    load_cols<TT, N>(old, row, c, a.width);
+    load_cols<TT, N>(f, row, c, a.width);
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = fmaf(s[i], a.scale, old[i]);
+    for (int i = 0; i < N; ++i) f[i] = fmaf(s[i], a.scale, f[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] *= a.scale;
+    for (int i = 0; i < N; ++i) f[i] = s[i] * a.scale;
   }
-  store_cols<TT, N>(row, c, a.width, s);
+  store_cols<TT, N, NT>(row, c, a.width, f);
+}
+template <int N>
+__device__ inline void write_part(const SumArgs& a, int64_t tile, int which, int c, const float (&s)[N]) {
+  float* to = a.partial + (tile * 2 + which) * a.part_ld + c;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) *reinterpret_cast<f32x4*>(to + i) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
 }
 
-// Tokens of at most kLong rows: 64 of them a workgroup, a wavefront for kWave * N columns.
-template <typename TT, typename TY>
-__global__ void __launch_bounds__(kThreads) sums_kernel(SumArgs a) {
-  constexpr int N = kCols<TY>;
+// Counts, and zeros for the tokens that do not occur, of 64 tokens.
+template <typename TT, typename TY, bool NT>
+__device__ inline void fill(const SumArgs& a, int group) {
+  constexpr int N = kCols<TT, TY>;
   __shared__ int64_t start[kWave + 1];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kWave;
-  if (wave == 0) {
-    start[lane] = first_at(a.keys, a.tokens, static_cast<uint32_t>(min(v0 + lane, static_cast<int64_t>(a.vocab))));
-    if (lane == 0) start[kWave] = first_at(a.keys, a.tokens, static_cast<uint32_t>(min(v0 + kWave, static_cast<int64_t>(a.vocab))));
-  }
+  const int64_t v0 = static_cast<int64_t>(group) * kWave;
+  for (int i = threadIdx.x; i <= kWave; i += blockDim.x)
+    start[i] = first_at(a.keys, a.tokens, static_cast<uint32_t>(min(v0 + i, static_cast<int64_t>(a.vocab))));
   __syncthreads();
-  if (a.counts && blockIdx.y == 0 && wave == 0 && v0 + lane < a.vocab)
-    a.counts[v0 + lane] = static_cast<int32_t>(start[lane + 1] - start[lane]);
-  const int c = ((blockIdx.y * (kThreads / kWave) + wave) * kWave + lane) * N;
+  if (a.counts && blockIdx.y == 0 && threadIdx.x < kWave && v0 + threadIdx.x < a.vocab)
+    a.counts[v0 + threadIdx.x] = static_cast<int32_t>(start[threadIdx.x + 1] - start[threadIdx.x]);
+  if (a.accumulate) return;
+  const float zero[N] = {};
+  for (int i = blockIdx.y; i < kWave && v0 + i < a.vocab; i += gridDim.y)        // whole rows, one after the other
+    if (start[i] == start[i + 1])
+      for (int c = threadIdx.x * N; c < a.width; c += blockDim.x * N) store_cols<TT, N, NT>(a.grad + (v0 + i) * a.grad_ld, c, a.width, zero);
+}
+
+// A tile of sorted positions a workgroup (further ones fill), kAhead rows asked for before they are
+// added.  Part 0 of a tile is the run that began before it, part 1 the one that
+// goes on after it (a run that does both is part 0).
+template <typename TT, typename TY, bool NT>
+__global__ void __launch_bounds__(kThreads) sums_kernel(SumArgs a) {
+  constexpr int N = kCols<TT, TY>;
+  if (static_cast<int>(blockIdx.x) >= a.tiles) return fill<TT, TY, NT>(a, blockIdx.x - a.tiles);
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tile, t1 = min(t0 + a.tile, a.tokens);
   if (c >= a.width) return;
-  for (int i = 0; i < kWave && v0 + i < a.vocab; ++i) {
-    const int64_t p0 = start[i], p1 = start[i + 1];
-    if (p1 - p0 > kLong || (p1 == p0 && a.accumulate)) continue;
-    float s[N];
+  const uint32_t none = static_cast<uint32_t>(a.vocab);
+  float s[N] = {};
+  uint32_t run = a.keys[t0];
+  bool head = t0 > 0 && a.keys[t0 - 1] == run;        // the run began before the tile
+  for (int64_t p0 = t0; p0 < t1 && run != none; p0 += kAhead) {
+    float f[kAhead][N];
+    uint32_t key[kAhead];
 #pragma unroll
-    for (int e = 0; e < N; ++e) s[e] = 0.f;
-    for (int64_t p = p0; p < p1; ++p) add_row<TY, N>(s, a.dy + a.perm[p] * a.dy_ld, c, a.width);
-    write_sum<TT, N>(a, v0 + i, c, s);
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t p = min(p0 + j, t1 - 1);
+      key[j] = a.keys[p];
+      load_cols<TY, N, NT>(f[j], a.dy + a.perm[p] * a.dy_ld, c, a.width);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (p0 + j >= t1) break;
+      if (key[j] != run) {
+        if (head) write_part<N>(a, blockIdx.x, 0, c, s);
+        else write_sum<TT, N, NT>(a, run, c, s);
+        head = false;
+        run = key[j];
+        if (run == none) break;                       // what is left are positions without a token
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = f[j][i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] += f[j][i];
+      }
+    }
   }
+  if (run == none) return;
+  if (head) write_part<N>(a, blockIdx.x, 0, c, s);
+  else if (t1 < a.tokens && a.keys[t1] == run) write_part<N>(a, blockIdx.x, 1, c, s);
+  else write_sum<TT, N, NT>(a, run, c, s);
 }
 
-// Where a token's rows lie, and whether they are left to the tiles.
-struct Run {
-  int64_t p0, p1;
-  __device__ Run(const SumArgs& a, uint32_t v) : p0(first_at(a.keys, a.tokens, v)), p1(first_at(a.keys, a.tokens, v + 1)) {}
-  __device__ bool by_tiles() const { return p1 - p0 > kLong; }
-};
-
-// A tile holds rows of at most two tokens of more than kLong: of its first
-// position's, whose sum goes to place 0, and of its last one's, to place 1.
-template <typename TY>
-__global__ void __launch_bounds__(kThreads) tiles_kernel(SumArgs a) {
-  constexpr int N = kCols<TY>;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kLong, t1 = min(t0 + kLong, a.tokens);
-  const int c = (blockIdx.y * kThreads + threadIdx.x) * N;
-  const uint32_t tokens[2] = {a.keys[t0], a.keys[t1 - 1]};
-  for (int which = 0; which < 2; ++which) {
-    const uint32_t v = tokens[which];
-    if (v >= static_cast<uint32_t>(a.vocab) || (which == 1 && v == tokens[0])) continue;
-    const Run r(a, v);
-    if (!r.by_tiles() || c >= a.width) continue;
-    float s[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) s[e] = 0.f;
-    const int64_t p1 = min(r.p1, t1);
-#pragma unroll 4
-    for (int64_t p = max(r.p0, t0); p < p1; ++p) add_row<TY, N>(s, a.dy + a.perm[p] * a.dy_ld, c, a.width);
-    float* to = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + which) * a.width;
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (c + e < a.width) to[c + e] = s[e];
-  }
-}
-
-// The sums of the tokens of more than kLong rows that begin in this tile.
-template <typename TT, typename TY>
+// The sum of the run that begins in a tile and goes on after it; further workgroups fill.
+template <typename TT, typename TY, bool NT>
 __global__ void __launch_bounds__(kThreads) join_kernel(SumArgs a) {
-  constexpr int N = kCols<TY>;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kLong, t1 = min(t0 + kLong, a.tokens);
-  const int c = (blockIdx.y * kThreads + threadIdx.x) * N;
-  const uint32_t v = a.keys[t1 - 1];         // one that begins here has rows to the tile's end, or is no long one
-  if (v >= static_cast<uint32_t>(a.vocab)) return;
-  const Run r(a, v);
-  if (!r.by_tiles() || r.p0 < t0 || c >= a.width) return;
+  constexpr int N = kCols<TT, TY>;
+  if (static_cast<int>(blockIdx.x) >= a.tiles) return fill<TT, TY, NT>(a, blockIdx.x - a.tiles + a.fill_first);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tile, t1 = t0 + a.tile;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
+  if (t1 >= a.tokens || c >= a.width) return;
+  const uint32_t v = a.keys[t1 - 1];
+  if (v == static_cast<uint32_t>(a.vocab) || a.keys[t1] != v || (a.keys[t0] == v && t0 > 0 && a.keys[t0 - 1] == v)) return;
+  const int64_t last = (first_at(a.keys, a.tokens, v + 1) - 1) / a.tile;
   float s[N];
+  const float* from = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * a.part_ld + c;
 #pragma unroll
-  for (int e = 0; e < N; ++e) s[e] = 0.f;
-  const int64_t last = (r.p1 - 1) / kLong;
-  for (int64_t tile = blockIdx.x; tile <= last; ++tile) {
-    const int which = tile == static_cast<int64_t>(blockIdx.x) && a.keys[t0] != v ? 1 : 0;
-    const float* from = a.partial + (tile * 2 + which) * a.width;
+  for (int i = 0; i < N; ++i) s[i] = from[i];
+  int64_t tile = blockIdx.x + 1;
+  for (; tile + kAhead <= last + 1; tile += kAhead) {
+    f32x4 f[kAhead][N / 4];
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (c + e < a.width) s[e] += from[c + e];
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q)
+        f[j][q] = *reinterpret_cast<const f32x4*>(a.partial + (tile + j) * 2 * a.part_ld + c + 4 * q);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] += f[j][i / 4][i % 4];
   }
-  write_sum<TT, N>(a, v, c, s);
+  for (; tile <= last; ++tile) {
+    const float* f = a.partial + tile * 2 * a.part_ld + c;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += f[i];
+  }
+  write_sum<TT, N, NT>(a, v, c, s);
 }
 
 template <typename F>
@@ -405,12 +512,16 @@ kfac_status_t launch_embedding_lookup(const kfac_embedding_t& e, char* ws, hipSt
     using TT = decltype(tt);
     using TY = decltype(ty);
     const int64_t most = 1 << 16;
-    if (e.width <= kWave * kCols<TY>) {
+    if (e.width <= kWave * Elem<TY>::VE) {
       const int64_t n = std::min<int64_t>((e.tokens + 3) / 4, most);
-      hipLaunchKernelGGL((lookup_kernel<TT, TY, kWave>), dim3(static_cast<uint32_t>(n)), dim3(kThreads), 0, st, a);
+      hipLaunchKernelGGL((lookup_kernel<TT, TY, kWave, false>), dim3(static_cast<uint32_t>(n)), dim3(kThreads), 0, st, a);
     } else {
       const int64_t n = std::min<int64_t>(e.tokens, most);
-      hipLaunchKernelGGL((lookup_kernel<TT, TY, kThreads>), dim3(static_cast<uint32_t>(n)), dim3(kThreads), 0, st, a);
+      // rows that do not fit the memory-side cache go past it: what is read again are the table's
+      if (e.tokens * e.width > kCacheBytes / 2 / static_cast<int64_t>(sizeof(TY)))
+        hipLaunchKernelGGL((lookup_kernel<TT, TY, kThreads, true>), dim3(static_cast<uint32_t>(n)), dim3(kThreads), 0, st, a);
+      else
+        hipLaunchKernelGGL((lookup_kernel<TT, TY, kThreads, false>), dim3(static_cast<uint32_t>(n)), dim3(kThreads), 0, st, a);
     }
     return hipGetLastError() == hipSuccess ? KFAC_OK : KFAC_ERR_HIP;
   });
@@ -431,6 +542,9 @@ kfac_status_t launch_embedding_grad(const kfac_embedding_t& e, char* ws, hipStre
   a.accumulate = e.accumulate;
   a.scale = e.scale;
   a.partial = reinterpret_cast<float*>(ws + r.partial);
+  a.part_ld = static_cast<int64_t>(part_ld(e.width));
+  a.tile = sum_tile(e.tokens);
+  a.tiles = static_cast<int32_t>((e.tokens + a.tile - 1) / a.tile);
 
   SortArgs s{};
   s.ids = e.ids;
@@ -442,7 +556,17 @@ kfac_status_t launch_embedding_grad(const kfac_embedding_t& e, char* ws, hipStre
   s.bits = plan.bits;
   s.tiles = plan.tiles;
   s.flags = reinterpret_cast<uint32_t*>(ws);
-  for (int pass = 0; pass < plan.passes && e.tokens > 0; ++pass) {
+  // positions that fit one workgroup's LDS: one launch in place of two a pass (5003 positions: 22 -> ... us)
+  const bool small = e.tokens <= kSmall;
+  if (small && e.tokens > 0) {
+    s.keys_out = reinterpret_cast<uint32_t*>(ws + r.keys[0]);
+    s.perm_out = reinterpret_cast<uint32_t*>(ws + r.perm[0]);
+    hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(kSmallThreads), 0, st, s, plan.passes);
+    if (hipGetLastError() != hipSuccess) return KFAC_ERR_HIP;
+    a.keys = s.keys_out;
+    a.perm = s.perm_out;
+  }
+  for (int pass = 0; pass < plan.passes && !small; ++pass) {
     const int to = pass & 1;
     s.shift = pass * plan.bits;
     s.keys = reinterpret_cast<const uint32_t*>(ws + r.keys[to ^ 1]);
@@ -464,15 +588,23 @@ kfac_status_t launch_embedding_grad(const kfac_embedding_t& e, char* ws, hipStre
   return by_types(e, [&](auto tt, auto ty) -> kfac_status_t {
     using TT = decltype(tt);
     using TY = decltype(ty);
-    constexpr int per = kThreads * kCols<TY>;
-    const uint32_t slabs = static_cast<uint32_t>((static_cast<int64_t>(e.width) + per - 1) / per);
+    const int64_t vectors = (static_cast<int64_t>(e.width) + kCols<TT, TY> - 1) / kCols<TT, TY>;
+    const uint32_t slabs = static_cast<uint32_t>((vectors + kThreads - 1) / kThreads);
+    const uint32_t threads = static_cast<uint32_t>(((vectors + slabs - 1) / slabs + kWave - 1) / kWave * kWave);
     const uint32_t groups = static_cast<uint32_t>((static_cast<int64_t>(e.vocab) + kWave - 1) / kWave);
-    hipLaunchKernelGGL((sums_kernel<TT, TY>), dim3(groups, slabs), dim3(kThreads), 0, st, a);
-    if (e.tokens > kLong) {
-      const uint32_t tiles = static_cast<uint32_t>((e.tokens + kLong - 1) / kLong);
-      hipLaunchKernelGGL(tiles_kernel<TY>, dim3(tiles, slabs), dim3(kThreads), 0, st, a);
-      hipLaunchKernelGGL((join_kernel<TT, TY>), dim3(tiles, slabs), dim3(kThreads), 0, st, a);
-    }
+    // The sums wait for rows and the joins for parts, the fills only write: half of
+    // them beside each.
+    const uint32_t beside = a.tiles ? groups / 2 : 0;
+    a.fill_first = static_cast<int32_t>(beside);
+    // dy and the gradient past the memory-side cache where they do not fit it
+    const bool past = (e.tokens * static_cast<int64_t>(sizeof(TY)) + e.vocab * static_cast<int64_t>(sizeof(TT))) * e.width > kCacheBytes;
+    auto go = [&](auto nt) {
+      constexpr bool NT = decltype(nt)::value;
+      if (a.tiles) hipLaunchKernelGGL((sums_kernel<TT, TY, NT>), dim3(a.tiles + beside, slabs), dim3(threads), 0, st, a);
+      hipLaunchKernelGGL((join_kernel<TT, TY, NT>), dim3(a.tiles + groups - beside, slabs), dim3(threads), 0, st, a);
+    };
+    if (past) go(std::true_type{});
+    else go(std::false_type{});
     return hipGetLastError() == hipSuccess ? KFAC_OK : KFAC_ERR_HIP;
   });
 }
