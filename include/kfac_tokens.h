@@ -44,7 +44,7 @@ enum { KFAC_TOK_SAMPLE = 0, KFAC_TOK_EMBEDDING = 1 };
  *     n_m   those with w >= min_p.
  * The token is the first column, by number, at which the running sum of the
  * kept w exceeds u times their whole sum.  T = 0 (any T below 1e-6) keeps the
- * first of the order alone.  logp is the token's log-probability in the whole
+ * first of the order alone; a T above 1e30 counts as 1e30.  logp is the token's log-probability in the whole
  * row, (x[token] - M) / T - log sum w (at T = 0 that of T = 1): what
  * kfac_token_logp gives at logit_scale = 1 / T.  Columns of minus infinity are
  * never kept; a row of nothing else has token -1, logp 0 and kept 0.

@@ -3,22 +3,33 @@
 // With M the row's maximum, w[i] = exp((x[i] - M) / T), and columns ordered by
 // falling x, equal ones by rising number, the kept columns are a prefix of that
 // order: all columns above one border (x, number), which is what is looked for.
-// No row is sorted.  One workgroup a row:
+// No row is sorted.  One workgroup a row, which is read once, into registers:
 //
-//   1. the row is read once, into registers, with its maximum;
-//   2. for top_k a histogram of counts, for top_p one of masses, over 1024 bins
-//      of (M - x) / T: the bin in which the border lies;
-//   3. that bin's columns, a few hundred at most in practice, are put in a list
-//      and each finds its place in the order by comparison with the others (a
-//      bin with more is narrowed by digits of (x, number) first);
-//   4. sums of the kept w, a column block at a time, in the columns' order, and
-//      the token in the block where u falls.
+//   top_k  The k-th largest of the threads' own maxima is at most the row's k-th
+//          largest: the columns from there on, hardly more than k, are put in a
+//          list, where each finds its place by comparison with the others.  The
+//          draw is made in the list.
+//   top_p  Two histograms of float32 masses, over 32 bins of (M - x) / T and over 32
+//          parts of the bin in which the border lies, say in which part it is; one
+//          pass then takes the exact masses: of all columns, of those above the part
+//          by blocks of columns, and a list of the part's.  Exact sums say whether
+//          the border is in the list, where each column finds its place by
+//          comparison.  The draw goes through the blocks' sums to a block, and
+//          through the block to a column.
+//   neither  the exact masses by blocks, and the draw.
+//
+// Rows that these do not settle (long runs of equal logits, a k beyond half the
+// threads, a border among the unlikeliest columns) take histograms of exact masses
+// and counts, narrowed by digits of (x, number) until a list holds what is left.
 //
 // w is held as a whole multiple of 2^-44: sums of integers have no rounding and
 // no order, so that LDS atomics add them, and a border or a draw is decided as
 // in 64-bit arithmetic.  It is formed in 64 bits (20 instructions a column);
 // only the log-probability's sum over columns that are not kept takes the
-// hardware's exp, 2^-22 off.
+// hardware's exp, 2^-22 off, and the first histograms, which decide nothing.  Those
+// are each thread's own, 32 words of LDS 4 NT bytes apart: an LDS atomic on float32
+// took 190 cycles a wavefront (100257 columns: 126 us), a read, an addition and a
+// write take ... .
 #include "tokens.h"
 
 #include <cmath>
@@ -31,7 +42,6 @@ constexpr int kBins = 1024;
 constexpr double kLog2e = 1.4426950408889634;
 constexpr float kGreedy = 1e-6f;          // temperatures below this keep the maximum alone
 constexpr float kBinsPerOctave = 16.f;    // 1024 bins reach 2^-64 of the maximum's weight
-constexpr int kMassBits = 44;
 
 struct SampleArgs {
   const char* x;
@@ -65,12 +75,14 @@ __device__ inline Border border_of(uint64_t place) {
           static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(place))};
 }
 
-// 2^z in multiples of 2^-44, z <= 0: e^(r ln 2) as its series to the 11th power
-// (|r| <= 1/2: 7e-15 of it is left out), and 2^52 added so that the significand's
-// low bits are the integer.
+// 2^z in multiples of 2^-44, z <= 0: z's nearest integer is left in the low bits by
+// adding 1.5 2^52; e^(r ln 2) is its series to the 11th power (|r| <= 1/2: 7e-15 of
+// it is left out); and 2^52 is added so that the significand's low bits are the
+// integer.
 __device__ inline uint64_t mass_of(double z) {
+  constexpr double shift = 6755399441055744.0;
   z = fmax(z, -60.0);
-  const double n = rint(z), r = z - n;
+  const double t = z + shift, r = z - (t - shift);
   double e = 4.44553827187081e-10;                 // ln2^k / k!, k = 11 .. 1
   e = fma(e, r, 7.054911620801121e-09);
   e = fma(e, r, 1.0178086009239696e-07);
@@ -83,19 +95,24 @@ __device__ inline uint64_t mass_of(double z) {
   e = fma(e, r, 0.2402265069591007);
   e = fma(e, r, 0.6931471805599453);
   e = fma(e, r, 1.0);
-  const double scaled = ldexp(e, static_cast<int>(n) + kMassBits) + 4503599627370496.0;
+  // times 2^n in its exponent
+  const uint64_t bits = __builtin_bit_cast(uint64_t, e) + (__builtin_bit_cast(uint64_t, t) << 52);
+  const double scaled = fma(__builtin_bit_cast(double, bits), 17592186044416.0, 4503599627370496.0);
   return __builtin_bit_cast(uint64_t, scaled) - 0x4330000000000000ull;
 }
 
-// The row: vectors of 16 bytes, NV a thread in registers, the others read again.
-template <typename T, int NT, int NV>
+// The row: vectors of 16 bytes.  Held in registers where a thread has one (HELD);
+// longer rows are read again by each pass, from the caches, two vectors a thread
+// ahead.  (Rows of up to 16 vectors a thread in registers left the passes too few:
+// 1023 x 100257 with top_p 961 us, of which most were moves and spills.)
+template <typename T, int NT, bool HELD>
 struct Row {
   static constexpr int VE = Elem<T>::VE;
   const char* x;
   int nfull, ntail, nvec;
-  u32x4 v[NV];
+  u32x4 v;
 
-  __device__ u32x4 load(int idx) const {
+  __device__ __forceinline__ u32x4 load(int idx) const {
     u32x4 r{Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf};
     if (idx < nfull) r = load16(x + static_cast<int64_t>(idx) * 16);
     else if (idx == nfull && ntail) {
@@ -107,63 +124,56 @@ struct Row {
     }
     return r;
   }
-  __device__ void fill(const char* row, int vocab) {
+  __device__ __forceinline__ void fill(const char* row, int vocab) {
     x = row;
     nfull = vocab / VE;
     ntail = vocab % VE;
     nvec = nfull + (ntail != 0);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = load(j * NT + static_cast<int>(threadIdx.x));
+    if constexpr (HELD) v = load(static_cast<int>(threadIdx.x));
   }
   __device__ int blocks() const { return (nvec + NT - 1) / NT; }
-  // f(vector, block) over the thread's vectors in the columns' order.
+  // f(vector, block) over the thread's vectors in the columns' order; every lane of a
+  // wavefront is there (absent columns are minus infinity).
   template <typename F>
-  __device__ void each(F f) const {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (j * NT < nvec) f(v[j], j);
-    for (int j = NV; j * NT < nvec; ++j) f(load(j * NT + static_cast<int>(threadIdx.x)), j);
-  }
-  // The same for long bodies, which are laid out CH times and not NV times: the
-  // registers move round.
-  template <typename F>
-  __device__ void each_long(F f) {
-    constexpr int CH = NV < 4 ? NV : 4;
+  __device__ __forceinline__ void each(F f) const {
+    if constexpr (HELD) {
+      f(v, 0);
+    } else {
+      const int tid = static_cast<int>(threadIdx.x), n = blocks();
+      u32x4 a = load(tid), b = load(NT + tid);
 #pragma unroll 1
-    for (int j0 = 0; j0 < NV; j0 += CH) {
-#pragma unroll
-      for (int j = 0; j < CH; ++j)
-        if ((j0 + j) * NT < nvec) f(v[j], j0 + j);
-      if constexpr (NV > CH) {
-        u32x4 t[CH];
-#pragma unroll
-        for (int j = 0; j < CH; ++j) t[j] = v[j];
-#pragma unroll
-        for (int j = 0; j + CH < NV; ++j) v[j] = v[j + CH];
-#pragma unroll
-        for (int j = 0; j < CH; ++j) v[NV - CH + j] = t[j];
+      for (int j = 0; j < n; j += 2) {
+        const u32x4 c = load((j + 2) * NT + tid), d = load((j + 3) * NT + tid);
+        f(a, j);
+        if (j + 1 < n) f(b, j + 1);
+        a = c;
+        b = d;
       }
     }
-    for (int j = NV; j * NT < nvec; ++j) f(load(j * NT + static_cast<int>(threadIdx.x)), j);
   }
   __device__ int column(int j, int i) const { return (j * NT + static_cast<int>(threadIdx.x)) * VE + i; }
 };
+
+constexpr int kOwn = 32;                  // bins of a thread's own histogram
+template <int NT>
+constexpr int kList = 4 * NT;             // listed columns: place and weight, in the histograms' LDS
 
 template <int NT>
 struct Shared {
   static constexpr int NW = NT / kWave;
   uint64_t mass[kBins];
-  uint64_t place[NT], weight[NT];         // a bin's columns
   uint32_t count[kBins];
   uint64_t wave_mass[NW];
   uint32_t wave_count[NW];
   uint64_t before_mass, place_min, total_mass;
   uint32_t before_count, bin, inside, listed, total_count;
-  float fmax[NW];
+  float fmax[NW], hist[kOwn];
   int fbad[NW];
   double rest[NW];
   uint64_t chosen_base;
   int32_t chosen_block;
+  uint64_t border, above_mass, list_mass;
+  uint32_t above_count, chosen;
 };
 
 // What a row's columns are compared and weighed by.
@@ -180,7 +190,7 @@ struct Scale {
 // running count reaches k, or the running mass reaches `goal` of all (by_mass).
 // Returns false where all columns together do not pass it.
 template <int NT>
-__device__ bool find_bin(Shared<NT>& s, int n, bool by_mass, uint32_t k, double goal, bool first) {
+__device__ __forceinline__ bool find_bin(Shared<NT>& s, int n, bool by_mass, uint32_t k, double goal, bool first) {
   constexpr int PER = kBins / NT;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   uint32_t c[PER], csum = 0;
@@ -211,7 +221,7 @@ __device__ bool find_bin(Shared<NT>& s, int n, bool by_mass, uint32_t k, double 
   mb += ms - msum;
   if (first) {
     if (by_mass) goal = fmax(goal * static_cast<double>(mt), 0.5);
-    else if (ct <= k) return false;
+    else if (ct < k) return false;
   }
   __syncthreads();
 #pragma unroll
@@ -233,7 +243,7 @@ __device__ bool find_bin(Shared<NT>& s, int n, bool by_mass, uint32_t k, double 
 }
 
 template <int NT>
-__device__ void clear_bins(Shared<NT>& s) {
+__device__ __forceinline__ void clear_bins(Shared<NT>& s) {
 #pragma unroll
   for (int b = threadIdx.x; b < kBins; b += NT) {
     s.count[b] = 0;
@@ -243,10 +253,11 @@ __device__ void clear_bins(Shared<NT>& s) {
 }
 
 // The border of top_k (by_mass false) or top_p among the columns within `in`.
-template <typename T, int NT, int NV>
-__device__ Border select(Shared<NT>& s, Row<T, NT, NV>& row, const Scale& sc, Border in, bool by_mass, uint32_t k,
+template <typename T, int NT, bool HELD>
+__device__ __forceinline__ Border select(Shared<NT>& s, uint64_t* list_place, Row<T, NT, HELD>& row, const Scale& sc, Border in, bool by_mass, uint32_t k,
                          double p) {
   constexpr int VE = Elem<T>::VE;
+  uint64_t* list_weight = list_place + kList<NT>;
   clear_bins<NT>(s);
   auto count = [&](u32x4 v, int j) {
 #pragma unroll
@@ -259,7 +270,7 @@ __device__ Border select(Shared<NT>& s, Row<T, NT, NV>& row, const Scale& sc, Bo
       }
     }
   };
-  row.each_long(count);
+  row.each(count);
   __syncthreads();
   if (!find_bin<NT>(s, kBins, by_mass, k, p, true)) return in;
   const double goal = by_mass ? fmax(p * static_cast<double>(s.total_mass), 0.5) : 0.0;
@@ -271,7 +282,7 @@ __device__ Border select(Shared<NT>& s, Row<T, NT, NV>& row, const Scale& sc, Bo
     __syncthreads();
     clear_bins<NT>(s);
     shift -= 8;
-    row.each_long([&](u32x4 v, int j) {
+    row.each([&](u32x4 v, int j) {
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
         const float x = Elem<T>::get(v, i);
@@ -301,24 +312,24 @@ __device__ Border select(Shared<NT>& s, Row<T, NT, NV>& row, const Scale& sc, Bo
       const uint64_t place = place_of(x, row.column(j, i));
       if (shift < 64 && (place >> shift) != digits) continue;
       const uint32_t at = atomicAdd(&s.listed, 1u);
-      s.place[at] = place;
+      list_place[at] = place;
     }
   });
   __syncthreads();
   const uint32_t n = s.inside;
   uint64_t mine = 0;
   if (threadIdx.x < n) {
-    mine = s.place[threadIdx.x];
-    if (by_mass) s.weight[threadIdx.x] = sc.mass(border_of(mine).x);
+    mine = list_place[threadIdx.x];
+    if (by_mass) list_weight[threadIdx.x] = sc.mass(border_of(mine).x);
   }
   __syncthreads();
   if (threadIdx.x < n) {
     uint32_t rank = s.before_count;
     uint64_t mass = s.before_mass;
     for (uint32_t f = 0; f < n; ++f) {
-      if (s.place[f] > mine) {
+      if (list_place[f] > mine) {
         ++rank;
-        if (by_mass) mass += s.weight[f];
+        if (by_mass) mass += list_weight[f];
       }
     }
     if (by_mass ? static_cast<double>(mass) < goal : rank < k)
@@ -326,6 +337,232 @@ __device__ Border select(Shared<NT>& s, Row<T, NT, NV>& row, const Scale& sc, Bo
   }
   __syncthreads();
   return border_of(s.place_min);
+}
+
+// Sum over the workgroup; every thread gets it.
+template <int NT>
+__device__ inline uint64_t all_sum(Shared<NT>& s, uint64_t v) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  v = wave_sum_u64(v);
+  __syncthreads();
+  if (lane == 0) s.wave_mass[wave] = v;
+  __syncthreads();
+  uint64_t t = 0;
+#pragma unroll
+  for (int w = 0; w < NT / kWave; ++w) t += s.wave_mass[w];
+  return t;
+}
+
+// What a row's draw gives.
+struct Drawn {
+  int32_t token, kept;
+  float x;
+  double sum;            // of all w
+};
+
+// top_k, with top_p and min_p on what it keeps, and the draw, in a list of the
+// columns from the k-th largest of the threads' maxima (`own`) on.  False where the
+// list does not hold them.
+template <typename T, int NT, bool HELD>
+__device__ __forceinline__ bool draw_of_few(Shared<NT>& s, uint64_t* place, Row<T, NT, HELD>& row, const Scale& sc, float own, uint32_t k, double p, float low,
+                            float u, Drawn* out) {
+  constexpr int VE = Elem<T>::VE;
+  const int tid = threadIdx.x;
+  uint64_t* weight_of = place + kList<NT>;
+  for (int b = tid; b < kBins; b += NT) s.count[b] = 0;
+  if (tid == 0) s.listed = 0;
+  __syncthreads();
+  if (own > -INFINITY) atomicAdd(&s.count[sc.bin(own)], 1u);
+  __syncthreads();
+  // (fewer than k threads have a column: all columns are listed)
+  const bool all = !find_bin<NT>(s, kBins, false, k, 0.0, true) || s.bin == kBins - 1;
+  const float reach = all ? 0.f : static_cast<float>(s.bin + 1);
+  const float cf = static_cast<float>(sc.c);
+  double rest = 0.0;
+  row.each([&](u32x4 v, int j) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float x = Elem<T>::get(v, i);
+      sum += __builtin_amdgcn_exp2f((x - sc.m) * cf);
+      if (((sc.m - x) * sc.bins < reach || all) && x > -INFINITY) {
+        const uint32_t at = atomicAdd(&s.listed, 1u);
+        if (at < NT) place[at] = place_of(x, row.column(j, i));
+      }
+    }
+    rest += static_cast<double>(sum);
+  });
+  rest = wave_sum(rest);
+  if ((tid & (kWave - 1)) == 0) s.rest[tid / kWave] = rest;
+  __syncthreads();
+  const uint32_t n = s.listed;
+  if (n > NT) return false;
+  uint64_t mine = 0, weight = 0;
+  float x = 0.f;
+  int32_t column = 0;
+  if (tid < n) {
+    mine = place[tid];
+    const Border b = border_of(mine);
+    x = b.x;
+    column = b.i;
+    weight = sc.mass(x);
+    weight_of[tid] = weight;
+  }
+  __syncthreads();
+  uint32_t rank = 0;
+  uint64_t before = 0;
+  if (tid < n) {
+    for (uint32_t f = 0; f < n; ++f) {
+      const bool first = place[f] > mine;
+      rank += first;
+      before += first ? weight_of[f] : 0;
+    }
+  }
+  bool keep = tid < n && rank < k;
+  if (p < 1.0) {
+    const double goal = fmax(p * static_cast<double>(all_sum<NT>(s, keep ? weight : 0)), 0.5);
+    keep = keep && static_cast<double>(before) < goal;
+  }
+  keep = keep && x >= low;
+  __syncthreads();
+  if (tid < n) weight_of[tid] = keep ? weight : 0;
+  const uint64_t total = all_sum<NT>(s, keep ? weight : 0);
+  const uint64_t count = all_sum<NT>(s, keep ? 1 : 0);
+  if (tid == 0) s.chosen = ~0u;
+  __syncthreads();
+  const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
+  if (keep) {
+    // the kept columns before this one: their places' low halves fall as the number rises
+    uint64_t run = 0;
+    for (uint32_t f = 0; f < n; ++f)
+      run += static_cast<uint32_t>(place[f]) > static_cast<uint32_t>(mine) ? weight_of[f] : 0;
+    if (run <= at && at < run + weight) s.chosen = tid;
+  }
+  __syncthreads();
+  if (tid == s.chosen) {
+    double sum = 0.0;
+    for (int w = 0; w < NT / kWave; ++w) sum += s.rest[w];
+    *out = {column, static_cast<int32_t>(count), x, sum};
+  }
+  return true;
+}
+
+// The border of top_p over the whole row, with the kept masses of the blocks of
+// columns in block_mass, their number in s.above_count and the whole row's mass in
+// s.total_mass.  False where the first histogram's bin does not hold it.
+template <typename T, int NT, bool HELD>
+__device__ __forceinline__ bool border_of_mass(Shared<NT>& s, float* own, uint64_t* block_mass, Row<T, NT, HELD>& row, const Scale& sc,
+                                               double p, int vocab, Border* out) {
+  constexpr int VE = Elem<T>::VE, LIST = kList<NT>;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const float cf = static_cast<float>(sc.c);
+  // columns of less than (1 - p) / vocab of the maximum's weight together weigh less
+  // than 1 - p: the border is above them, and the last bin is theirs
+  const float octaves = fminf(fmaxf(1.f + log2f(static_cast<float>(vocab)) - log2f(fmaxf(static_cast<float>(1.0 - p), 1e-9f)), 2.f), 60.f);
+  float width = cf * (static_cast<float>(kOwn - 1) / octaves), above = 0.f, mass_above = 0.f, goal = 0.f;
+  // twice: bins of (m - x) width, then parts of the bin [above, above + 1)
+#pragma unroll 1
+  for (int level = 0; level < 2; ++level) {
+    for (int i = 0; i < kOwn; ++i) own[i * NT + tid] = 0.f;
+    if (tid == 0) s.bin = kOwn;
+    __syncthreads();
+    const float coarse = width;
+    row.each([&](u32x4 v, int) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float d = sc.m - Elem<T>::get(v, i);
+        const float at = d * coarse;
+        if (level == 0 || (at >= above && at < above + 1.f)) {
+          const int b = static_cast<int>(fminf(level == 0 ? at : (at - above) * static_cast<float>(kOwn), static_cast<float>(kOwn - 1)));
+          own[b * NT + tid] += __builtin_amdgcn_exp2f(-d * cf);
+        }
+      }
+    });
+    __syncthreads();
+    // the bins' sums: NT / kOwn threads each
+    constexpr int PER = NT / kOwn;
+    float sum = 0.f;
+    for (int i = 0; i < NT / PER; ++i) sum += own[(tid / PER) * NT + i * PER + tid % PER];
+#pragma unroll
+    for (int d = 1; d < PER; d <<= 1) sum += __shfl_xor(sum, d);
+    if (tid % PER == 0) s.hist[tid / PER] = sum;
+    __syncthreads();
+    if (tid < kWave) {
+      const float mass = lane < kOwn ? s.hist[lane] : 0.f;
+      const float upto = wave_scan(mass) + mass_above;
+      if (level == 0) goal = static_cast<float>(p) * __shfl(upto, kWave - 1);
+      if (mass > 0.f && upto >= goal) atomicMin(&s.bin, static_cast<uint32_t>(lane));
+      if (lane < kOwn) s.hist[lane] = upto - mass;
+    }
+    __syncthreads();
+    const int bin = s.bin;
+    if (bin >= kOwn || (level == 0 && bin == kOwn - 1)) return false;
+    mass_above = s.hist[bin];
+    if (level == 0) above = static_cast<float>(bin);
+    else s.bin = bin;
+    __syncthreads();
+  }
+  const float part = static_cast<float>(s.bin);
+  if (tid == 0) s.listed = 0;
+  __syncthreads();
+  uint64_t* place = reinterpret_cast<uint64_t*>(own);
+  uint64_t* weight = place + LIST;
+  uint64_t all = 0;
+  uint32_t kept = 0;
+  row.each([&](u32x4 v, int j) {
+    uint64_t mass = 0;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float x = Elem<T>::get(v, i), at = (sc.m - x) * width;
+      const float in = fminf((at - above) * static_cast<float>(kOwn), static_cast<float>(kOwn - 1));
+      const uint64_t w = sc.mass(x);
+      all += w;
+      if (at < above || (at < above + 1.f && in < part)) {
+        mass += w;
+        ++kept;
+      } else if (at < above + 1.f && in < part + 1.f) {
+        const uint32_t to = atomicAdd(&s.listed, 1u);
+        if (to < LIST) place[to] = place_of(x, row.column(j, i));
+      }
+    }
+    const uint64_t sum = wave_sum_u64(mass);
+    if (lane == 0 && sum) atomicAdd(reinterpret_cast<unsigned long long*>(&block_mass[j]), static_cast<unsigned long long>(sum));
+  });
+  const uint64_t total = all_sum<NT>(s, all);
+  const uint64_t count = all_sum<NT>(s, kept);
+  uint64_t above_mass = 0;
+  for (int j = tid; j < row.blocks(); j += NT) above_mass += block_mass[j];
+  above_mass = all_sum<NT>(s, above_mass);
+  const uint32_t n = s.listed;
+  const double want = fmax(p * static_cast<double>(total), 0.5);
+  if (n > NT || !(static_cast<double>(above_mass) < want)) return false;
+  uint64_t mine = 0, own_mass = 0;
+  if (tid < n) {
+    mine = place[tid];
+    weight[tid] = own_mass = sc.mass(border_of(mine).x);
+  }
+  const uint64_t list_mass = all_sum<NT>(s, own_mass);
+  if (!(static_cast<double>(above_mass + list_mass) >= want)) return false;
+  if (tid == 0) s.place_min = ~0ull;
+  __syncthreads();
+  bool keep = false;
+  if (tid < n) {
+    uint64_t before = above_mass;
+    for (uint32_t f = 0; f < n; ++f) before += place[f] > mine ? weight[f] : 0;
+    keep = static_cast<double>(before) < want;
+    if (keep) {
+      atomicMin(reinterpret_cast<unsigned long long*>(&s.place_min), static_cast<unsigned long long>(mine));
+      atomicAdd(reinterpret_cast<unsigned long long*>(&block_mass[border_of(mine).i / (VE * NT)]), static_cast<unsigned long long>(own_mass));
+    }
+  }
+  const uint64_t listed = all_sum<NT>(s, keep ? 1 : 0);
+  if (tid == 0) {
+    s.above_count = static_cast<uint32_t>(count + listed);
+    s.total_mass = total;
+  }
+  __syncthreads();
+  *out = border_of(s.place_min);
+  return true;
 }
 
 // The least float whose weight is at least m (0 < m <= 1).
@@ -338,14 +575,17 @@ __device__ inline Border min_p_border(const Scale& sc, double m) {
   return {x, INT32_MAX};
 }
 
-template <typename T, int NT, int NV, bool CUT>
+template <typename T, int NT, bool HELD, bool CUT>
 __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   constexpr int VE = Elem<T>::VE, NW = NT / kWave;
   __shared__ Shared<NT> s;
-  extern __shared__ uint64_t block_mass[];        // kept mass of each block of NT vectors
+  extern __shared__ uint64_t block_mass[];         // kept mass of each block of NT vectors
+  __shared__ uint64_t lists[CUT ? kOwn * NT / 2 : 1];      // or the threads' histograms
+  float* histograms = reinterpret_cast<float*>(lists);
+  static_assert(kOwn * NT * sizeof(float) >= 2 * kList<NT> * sizeof(uint64_t));
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  Row<T, NT, NV> row;
+  Row<T, NT, HELD> row;
   row.fill(a.x + r * a.ldx, a.vocab);
   const int blocks = row.blocks();
   for (int j = tid; j < blocks; j += NT) block_mass[j] = 0;
@@ -356,7 +596,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   double p = a.row_p ? static_cast<double>(a.row_p[r]) : a.p, m = a.row_m ? static_cast<double>(a.row_m[r]) : a.m;
   int32_t k = a.row_k ? a.row_k[r] : a.k;
   const bool valid = u >= 0.f && u < 1.f && t >= 0.f && p == p && m == m;
-  const double inv_t = t < kGreedy ? 1.0 : 1.0 / (a.row_t ? static_cast<double>(t) : a.t);
+  const double inv_t = t < kGreedy ? 1.0 : 1.0 / fmin(a.row_t ? static_cast<double>(t) : a.t, 1e30);
   if (t < kGreedy) k = 1;
 
   // maximum, and whether every value is a number below infinity
@@ -370,6 +610,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
       top = fmaxf(top, x);
     }
   });
+  const float own = top;
   top = wave_max(top);
   const bool any_bad = __any(bad);
   if (lane == 0) {
@@ -399,42 +640,68 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   sc.c = kLog2e * inv_t;
   sc.bins = static_cast<float>(sc.c) * kBinsPerOctave;
   Border border{-INFINITY, -1};
+  bool summed = false;                       // block_mass and the count are there
   if constexpr (CUT) {
-    if (k > 0) border = select<T, NT, NV>(s, row, sc, border, false, static_cast<uint32_t>(k), 0.0);
-    if (p < 1.0 && k != 1) border = select<T, NT, NV>(s, row, sc, border, true, 0, p);
-    if (m > 0.0) {
-      const Border low = min_p_border(sc, fmin(m, 1.0));
-      if (low.x > border.x) border = low;
+    Border low{-INFINITY, -1};
+    if (m > 0.0) low = min_p_border(sc, fmin(m, 1.0));
+    if (k > 0 && k <= NT / 2) {
+      Drawn d;
+      d.token = -1;
+      if (draw_of_few<T, NT, HELD>(s, lists, row, sc, own, static_cast<uint32_t>(k), k == 1 ? 1.0 : p, low.x, u, &d)) {
+        if (d.token >= 0) {                  // the one thread that has it
+          a.token[r] = d.token;
+          a.logp[r] = static_cast<float>((static_cast<double>(d.x) - static_cast<double>(top)) * inv_t - log(d.sum));
+          a.kept[r] = d.kept;
+        }
+        return;
+      }
+      __syncthreads();
+    }
+    if (k > 0) border = select<T, NT, HELD>(s, lists, row, sc, border, false, static_cast<uint32_t>(k), 0.0);
+    if (p < 1.0 && k != 1) {
+      summed = k <= 0 && border_of_mass<T, NT, HELD>(s, histograms, block_mass, row, sc, p, a.vocab, &border);
+      if (!summed) border = select<T, NT, HELD>(s, lists, row, sc, border, true, 0, p);
+    }
+    if (low.x > border.x) {
+      border = low;
+      summed = false;
+    }
+    if (!summed) {
+      __syncthreads();
+      for (int j = tid; j < blocks; j += NT) block_mass[j] = 0;
+      __syncthreads();
     }
   }
 
   // the kept mass of each block of columns, the other columns' in 32-bit terms
-  const float cf = static_cast<float>(sc.c);
-  double rest = 0.0;
-  uint32_t kept = 0;
-  row.each_long([&](u32x4 v, int j) {
-    uint64_t mass = 0;
-    float others = 0.f;
+  if (!summed) {
+    const float cf = static_cast<float>(sc.c);
+    double rest = 0.0;
+    uint32_t kept = 0;
+    row.each([&](u32x4 v, int j) {
+      uint64_t mass = 0;
+      float others = 0.f;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float x = Elem<T>::get(v, i);
-      if (x > -INFINITY && (!CUT || border.keeps(x, row.column(j, i)))) {
-        mass += sc.mass(x);
-        ++kept;
-      } else if (CUT) {
-        others += __builtin_amdgcn_exp2f((x - top) * cf);
+      for (int i = 0; i < VE; ++i) {
+        const float x = Elem<T>::get(v, i);
+        if (x > -INFINITY && (!CUT || border.keeps(x, row.column(j, i)))) {
+          mass += sc.mass(x);
+          ++kept;
+        } else if (CUT) {
+          others += __builtin_amdgcn_exp2f((x - top) * cf);
+        }
       }
-    }
-    if (CUT) rest += static_cast<double>(others);
-    if (__any(mass != 0)) {
-      const uint64_t sum = wave_sum_u64(mass);
-      if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&block_mass[j]), static_cast<unsigned long long>(sum));
-    }
-  });
-  rest = wave_sum(rest);
-  uint32_t count = wave_scan(kept);
-  if (lane == kWave - 1) s.wave_count[wave] = count;
-  if (lane == 0) s.rest[wave] = rest;
+      if (CUT) rest += static_cast<double>(others);
+      if (__any(mass != 0)) {
+        const uint64_t sum = wave_sum_u64(mass);
+        if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&block_mass[j]), static_cast<unsigned long long>(sum));
+      }
+    });
+    rest = wave_sum(rest);
+    const uint32_t count = wave_scan(kept);
+    if (lane == kWave - 1) s.wave_count[wave] = count;
+    if (lane == 0) s.rest[wave] = rest;
+  }
   __syncthreads();
 
   // the block where u falls
@@ -452,7 +719,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
       }
       before = lane_of(upto, kWave - 1);
     }
-    if (lane == 0) s.total_mass = total;
+    if (lane == 0) s.list_mass = total;          // of the kept
   }
   __syncthreads();
   const int block = s.chosen_block;
@@ -486,12 +753,17 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
       }
     }
     uint32_t n = 0;
-    double others = 0.0;
-    for (int w = 0; w < NW; ++w) {
-      n += s.wave_count[w];
-      others += s.rest[w];
+    double sum = 0.0;
+    if (summed) {
+      n = s.above_count;
+      sum = static_cast<double>(s.total_mass) * 0x1p-44;
+    } else {
+      for (int w = 0; w < NW; ++w) {
+        n += s.wave_count[w];
+        sum += s.rest[w];
+      }
+      sum += static_cast<double>(s.list_mass) * 0x1p-44;
     }
-    const double sum = static_cast<double>(s.total_mass) * 0x1p-44 + others;
     a.token[r] = row.column(block, found);
     a.logp[r] = static_cast<float>((static_cast<double>(xt) - static_cast<double>(top)) * inv_t - log(sum));
     a.kept[r] = static_cast<int32_t>(n);
@@ -523,11 +795,12 @@ kfac_status_t launch_typed(const SampleArgs& a, int64_t rows, hipStream_t st) {
     }
     return KFAC_OK;
   };
-  if (nvec <= 256) return go(sample_kernel<T, 256, 1, CUT>, 256);
-  if (nvec <= 1024) return go(sample_kernel<T, 256, 4, CUT>, 256);
-  if (nvec <= 4096) return go(sample_kernel<T, 1024, 4, CUT>, 1024);
-  if (nvec <= 8192) return go(sample_kernel<T, 1024, 8, CUT>, 1024);
-  return go(sample_kernel<T, 1024, 16, CUT>, 1024);
+  // Wavefronts enough to fill the compute units with the rows that there are: a
+  // workgroup of 1024 threads a unit, or two of 512, or (short rows) many of 256.
+  if (nvec <= 256) return go(sample_kernel<T, 256, true, CUT>, 256);
+  if (nvec <= 1024) return go(sample_kernel<T, 256, false, CUT>, 256);
+  if (rows > 256) return go(sample_kernel<T, 512, false, CUT>, 512);
+  return go(sample_kernel<T, 1024, false, CUT>, 1024);
 }
 
 }  // namespace
