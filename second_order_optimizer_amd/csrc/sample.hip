@@ -156,14 +156,19 @@ struct Row {
 
 constexpr int kOwn = 32;                  // bins of a thread's own histogram
 template <int NT>
-constexpr int kList = 4 * NT;             // listed columns: place and weight, in the histograms' LDS
+constexpr int kList = 4 * NT;             // listed columns, in the histograms' LDS
+
+// A listed column and its mass: sixteen bytes, one read.
+struct alignas(16) Listed {
+  uint64_t place, mass;
+};
 
 template <int NT>
 struct Shared {
   static constexpr int NW = NT / kWave;
   uint64_t mass[kBins];
   uint32_t count[kBins];
-  uint64_t wave_mass[NW];
+  uint64_t wave_mass[NW], sums[3][NW];
   uint32_t wave_count[NW];
   uint64_t before_mass, place_min, total_mass;
   uint32_t before_count, bin, inside, listed, total_count;
@@ -252,12 +257,61 @@ __device__ __forceinline__ void clear_bins(Shared<NT>& s) {
   __syncthreads();
 }
 
+// Sums over the workgroup; every thread gets them.
+template <int NT, int N>
+__device__ __forceinline__ void all_sums(Shared<NT>& s, uint64_t (&v)[N]) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum_u64(v[i]);
+  __syncthreads();
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s.sums[i][wave] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    // a wavefront's lanes read the wavefronts' sums at once
+    v[i] = wave_sum_u64(lane < NT / kWave ? s.sums[i][lane] : 0);
+  }
+}
+template <int NT>
+__device__ __forceinline__ uint64_t all_sum(Shared<NT>& s, uint64_t v) {
+  uint64_t one[1] = {v};
+  all_sums<NT, 1>(s, one);
+  return one[0];
+}
+
+// Of a list of n columns: how many come before `mine` in the order, and their mass.
+__device__ __forceinline__ void before_in_list(const Listed* list, uint32_t n, uint64_t mine, uint32_t* rank, uint64_t* mass) {
+  uint32_t r = 0;
+  uint64_t m = 0;
+  uint32_t f = 0;
+  for (; f + 8 <= n; f += 8) {
+    Listed e[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) e[q] = list[f + q];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const bool first = e[q].place > mine;
+      r += first;
+      m += first ? e[q].mass : 0;
+    }
+  }
+  for (; f < n; ++f) {
+    const bool first = list[f].place > mine;
+    r += first;
+    m += first ? list[f].mass : 0;
+  }
+  *rank += r;
+  *mass += m;
+}
+
 // The border of top_k (by_mass false) or top_p among the columns within `in`.
 template <typename T, int NT, bool HELD>
-__device__ __forceinline__ Border select(Shared<NT>& s, uint64_t* list_place, Row<T, NT, HELD>& row, const Scale& sc, Border in, bool by_mass, uint32_t k,
+__device__ __forceinline__ Border select(Shared<NT>& s, Listed* list, Row<T, NT, HELD>& row, const Scale& sc, Border in, bool by_mass, uint32_t k,
                          double p) {
   constexpr int VE = Elem<T>::VE;
-  uint64_t* list_weight = list_place + kList<NT>;
   clear_bins<NT>(s);
   auto count = [&](u32x4 v, int j) {
 #pragma unroll
@@ -312,45 +366,26 @@ __device__ __forceinline__ Border select(Shared<NT>& s, uint64_t* list_place, Ro
       const uint64_t place = place_of(x, row.column(j, i));
       if (shift < 64 && (place >> shift) != digits) continue;
       const uint32_t at = atomicAdd(&s.listed, 1u);
-      list_place[at] = place;
+      list[at].place = place;
     }
   });
   __syncthreads();
   const uint32_t n = s.inside;
   uint64_t mine = 0;
   if (threadIdx.x < n) {
-    mine = list_place[threadIdx.x];
-    if (by_mass) list_weight[threadIdx.x] = sc.mass(border_of(mine).x);
+    mine = list[threadIdx.x].place;
+    list[threadIdx.x].mass = by_mass ? sc.mass(border_of(mine).x) : 0;
   }
   __syncthreads();
   if (threadIdx.x < n) {
     uint32_t rank = s.before_count;
     uint64_t mass = s.before_mass;
-    for (uint32_t f = 0; f < n; ++f) {
-      if (list_place[f] > mine) {
-        ++rank;
-        if (by_mass) mass += list_weight[f];
-      }
-    }
+    before_in_list(list, n, mine, &rank, &mass);
     if (by_mass ? static_cast<double>(mass) < goal : rank < k)
       atomicMin(reinterpret_cast<unsigned long long*>(&s.place_min), static_cast<unsigned long long>(mine));
   }
   __syncthreads();
   return border_of(s.place_min);
-}
-
-// Sum over the workgroup; every thread gets it.
-template <int NT>
-__device__ inline uint64_t all_sum(Shared<NT>& s, uint64_t v) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  v = wave_sum_u64(v);
-  __syncthreads();
-  if (lane == 0) s.wave_mass[wave] = v;
-  __syncthreads();
-  uint64_t t = 0;
-#pragma unroll
-  for (int w = 0; w < NT / kWave; ++w) t += s.wave_mass[w];
-  return t;
 }
 
 // What a row's draw gives.
@@ -364,11 +399,10 @@ struct Drawn {
 // columns from the k-th largest of the threads' maxima (`own`) on.  False where the
 // list does not hold them.
 template <typename T, int NT, bool HELD>
-__device__ __forceinline__ bool draw_of_few(Shared<NT>& s, uint64_t* place, Row<T, NT, HELD>& row, const Scale& sc, float own, uint32_t k, double p, float low,
+__device__ __forceinline__ bool draw_of_few(Shared<NT>& s, Listed* list, Row<T, NT, HELD>& row, const Scale& sc, float own, uint32_t k, double p, float low,
                             float u, Drawn* out) {
   constexpr int VE = Elem<T>::VE;
   const int tid = threadIdx.x;
-  uint64_t* weight_of = place + kList<NT>;
   for (int b = tid; b < kBins; b += NT) s.count[b] = 0;
   if (tid == 0) s.listed = 0;
   __syncthreads();
@@ -387,7 +421,7 @@ __device__ __forceinline__ bool draw_of_few(Shared<NT>& s, uint64_t* place, Row<
       sum += __builtin_amdgcn_exp2f((x - sc.m) * cf);
       if (((sc.m - x) * sc.bins < reach || all) && x > -INFINITY) {
         const uint32_t at = atomicAdd(&s.listed, 1u);
-        if (at < NT) place[at] = place_of(x, row.column(j, i));
+        if (at < NT) list[at].place = place_of(x, row.column(j, i));
       }
     }
     rest += static_cast<double>(sum);
@@ -401,41 +435,35 @@ __device__ __forceinline__ bool draw_of_few(Shared<NT>& s, uint64_t* place, Row<
   float x = 0.f;
   int32_t column = 0;
   if (tid < n) {
-    mine = place[tid];
+    mine = list[tid].place;
     const Border b = border_of(mine);
     x = b.x;
     column = b.i;
     weight = sc.mass(x);
-    weight_of[tid] = weight;
+    list[tid].mass = weight;
   }
   __syncthreads();
   uint32_t rank = 0;
   uint64_t before = 0;
-  if (tid < n) {
-    for (uint32_t f = 0; f < n; ++f) {
-      const bool first = place[f] > mine;
-      rank += first;
-      before += first ? weight_of[f] : 0;
-    }
-  }
+  if (tid < n) before_in_list(list, n, mine, &rank, &before);
   bool keep = tid < n && rank < k;
   if (p < 1.0) {
     const double goal = fmax(p * static_cast<double>(all_sum<NT>(s, keep ? weight : 0)), 0.5);
     keep = keep && static_cast<double>(before) < goal;
   }
   keep = keep && x >= low;
-  __syncthreads();
-  if (tid < n) weight_of[tid] = keep ? weight : 0;
-  const uint64_t total = all_sum<NT>(s, keep ? weight : 0);
-  const uint64_t count = all_sum<NT>(s, keep ? 1 : 0);
+  uint64_t sums[2] = {keep ? weight : 0, keep ? 1u : 0u};
+  all_sums<NT, 2>(s, sums);
+  const uint64_t total = sums[0], count = sums[1];
+  if (tid < n) list[tid] = {static_cast<uint32_t>(mine), keep ? weight : 0};      // in the columns' order from here on
   if (tid == 0) s.chosen = ~0u;
   __syncthreads();
   const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
   if (keep) {
     // the kept columns before this one: their places' low halves fall as the number rises
     uint64_t run = 0;
-    for (uint32_t f = 0; f < n; ++f)
-      run += static_cast<uint32_t>(place[f]) > static_cast<uint32_t>(mine) ? weight_of[f] : 0;
+    uint32_t rank_by_number = 0;
+    before_in_list(list, n, static_cast<uint32_t>(mine), &rank_by_number, &run);
     if (run <= at && at < run + weight) s.chosen = tid;
   }
   __syncthreads();
@@ -505,10 +533,10 @@ __device__ __forceinline__ bool border_of_mass(Shared<NT>& s, float* own, uint64
   const float part = static_cast<float>(s.bin);
   if (tid == 0) s.listed = 0;
   __syncthreads();
-  uint64_t* place = reinterpret_cast<uint64_t*>(own);
-  uint64_t* weight = place + LIST;
+  Listed* list = reinterpret_cast<Listed*>(own);
   uint64_t all = 0;
   uint32_t kept = 0;
+  uint64_t above_own = 0;
   row.each([&](u32x4 v, int j) {
     uint64_t mass = 0;
 #pragma unroll
@@ -522,24 +550,23 @@ __device__ __forceinline__ bool border_of_mass(Shared<NT>& s, float* own, uint64
         ++kept;
       } else if (at < above + 1.f && in < part + 1.f) {
         const uint32_t to = atomicAdd(&s.listed, 1u);
-        if (to < LIST) place[to] = place_of(x, row.column(j, i));
+        if (to < LIST) list[to].place = place_of(x, row.column(j, i));
       }
     }
+    above_own += mass;
     const uint64_t sum = wave_sum_u64(mass);
     if (lane == 0 && sum) atomicAdd(reinterpret_cast<unsigned long long*>(&block_mass[j]), static_cast<unsigned long long>(sum));
   });
-  const uint64_t total = all_sum<NT>(s, all);
-  const uint64_t count = all_sum<NT>(s, kept);
-  uint64_t above_mass = 0;
-  for (int j = tid; j < row.blocks(); j += NT) above_mass += block_mass[j];
-  above_mass = all_sum<NT>(s, above_mass);
+  uint64_t sums[3] = {all, kept, above_own};
+  all_sums<NT, 3>(s, sums);
+  const uint64_t total = sums[0], count = sums[1], above_mass = sums[2];
   const uint32_t n = s.listed;
   const double want = fmax(p * static_cast<double>(total), 0.5);
   if (n > NT || !(static_cast<double>(above_mass) < want)) return false;
   uint64_t mine = 0, own_mass = 0;
   if (tid < n) {
-    mine = place[tid];
-    weight[tid] = own_mass = sc.mass(border_of(mine).x);
+    mine = list[tid].place;
+    list[tid].mass = own_mass = sc.mass(border_of(mine).x);
   }
   const uint64_t list_mass = all_sum<NT>(s, own_mass);
   if (!(static_cast<double>(above_mass + list_mass) >= want)) return false;
@@ -548,7 +575,8 @@ __device__ __forceinline__ bool border_of_mass(Shared<NT>& s, float* own, uint64
   bool keep = false;
   if (tid < n) {
     uint64_t before = above_mass;
-    for (uint32_t f = 0; f < n; ++f) before += place[f] > mine ? weight[f] : 0;
+    uint32_t rank = 0;
+    before_in_list(list, n, mine, &rank, &before);
     keep = static_cast<double>(before) < want;
     if (keep) {
       atomicMin(reinterpret_cast<unsigned long long*>(&s.place_min), static_cast<unsigned long long>(mine));
@@ -580,9 +608,9 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   constexpr int VE = Elem<T>::VE, NW = NT / kWave;
   __shared__ Shared<NT> s;
   extern __shared__ uint64_t block_mass[];         // kept mass of each block of NT vectors
-  __shared__ uint64_t lists[CUT ? kOwn * NT / 2 : 1];      // or the threads' histograms
+  __shared__ Listed lists[CUT ? kOwn * NT / 4 : 1];        // or the threads' histograms
   float* histograms = reinterpret_cast<float*>(lists);
-  static_assert(kOwn * NT * sizeof(float) >= 2 * kList<NT> * sizeof(uint64_t));
+  static_assert(kOwn * NT * sizeof(float) >= kList<NT> * sizeof(Listed));
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   Row<T, NT, HELD> row;
