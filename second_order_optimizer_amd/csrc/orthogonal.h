@@ -62,6 +62,13 @@ inline PolyBound poly_of(const float* coef, double rho) {
   return r;
 }
 
+// Matrices with a side of at most this run on d x d matrices in one workgroup each.
+constexpr int kOrthSmall = 64;
+inline bool orth_is_small(const OrthTask& t) { return std::min(t.rows, t.cols) <= kOrthSmall; }
+size_t orth_small_bytes(const std::vector<OrthTask>& tasks);
+kfac_status_t launch_orth_small(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how, const OrthStep& step,
+                                char* regions, uint32_t* flags, hipStream_t st);
+
 size_t orth_workspace_bytes(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how);
 kfac_status_t launch_orthogonal(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how, const OrthStep& step,
                                 char* ws, hipStream_t st);

@@ -25,8 +25,7 @@
 // Layout.  Planes are row-major, both sides padded with zeros to whole tiles,
 // which every product keeps at zero: no bounds checks outside the first and last
 // pass.
-#include "orthogonal.h"
-#include "objectives.h"
+#include "orthogonal_load.h"
 
 #include <algorithm>
 #include <cmath>
@@ -82,26 +81,6 @@ __device__ inline int find(const PrepBatch& b, int blk) {
   return i;
 }
 
-// 8 values of a row from column c on, those past its `cols` columns 0.
-__device__ inline void load8(float (&f)[8], const void* row, int c, int cols, int bf16) {
-  if (c + 8 <= cols) {
-    if (bf16) {
-      const u32x4 v = load16(static_cast<const unsigned short*>(row) + c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = Elem<__bf16>::get(v, e);
-    } else {
-      const u32x4 v0 = load16(static_cast<const float*>(row) + c), v1 = load16(static_cast<const float*>(row) + c + 4);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(e < 4 ? v0[e & 3] : v1[e & 3]);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      f[e] = c + e >= cols ? 0.f
-             : bf16        ? bf16_bits_to_float(static_cast<const unsigned short*>(row)[c + e])
-                           : static_cast<const float*>(row)[c + e];
-  }
-}
 __device__ inline const void* row_at(const PrepProb& P, int64_t at) {
   return P.bf16 ? static_cast<const void*>(static_cast<const unsigned short*>(P.x) + at)
                 : static_cast<const void*>(static_cast<const float*>(P.x) + at);
@@ -915,18 +894,27 @@ size_t partial_bytes(const Cut& c) { return static_cast<size_t>(c.shares) * 2 * 
 
 }  // namespace
 
-size_t orth_workspace_bytes(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how) {
-  size_t partial = 0;
+size_t orth_workspace_bytes(const std::vector<OrthTask>& all, const kfac_orthogonal_t& how) {
+  std::vector<OrthTask> small, tasks;
+  for (const OrthTask& t : all) (orth_is_small(t) ? small : tasks).push_back(t);
+  size_t partial = orth_small_bytes(small);
   for (const Group& g : groups_of(tasks, how.products == KFAC_PRODUCTS_FULL ? 2 : 1))
-    for (const Cut& c : {g.gram, g.poly, g.next}) partial = std::max(partial, partial_bytes(c));
+    for (const Cut& c : {g.gram, g.poly, g.next}) partial = std::max(partial, partial_bytes(c));      // one after the other
   return plan(tasks, how, nullptr) + partial;
 }
 
-kfac_status_t launch_orthogonal(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how, const OrthStep& step,
+kfac_status_t launch_orthogonal(const std::vector<OrthTask>& all, const kfac_orthogonal_t& how, const OrthStep& step,
                                 char* ws, hipStream_t st) {
+  std::vector<OrthTask> small, tasks;
+  for (const OrthTask& t : all) (orth_is_small(t) ? small : tasks).push_back(t);
   const int planes = how.products == KFAC_PRODUCTS_FULL ? 2 : 1;
   std::vector<Region> regions;
-  float* partial = reinterpret_cast<float*>(ws + plan(tasks, how, &regions));
+  char* rest = ws + plan(tasks, how, &regions);
+  float* partial = reinterpret_cast<float*>(rest);
+  if (!small.empty()) {
+    const kfac_status_t r = launch_orth_small(small, how, step, rest, reinterpret_cast<uint32_t*>(ws), st);
+    if (r != KFAC_OK || tasks.empty()) return r;
+  }
   int last_bits = 0;
   const std::vector<StepScale> scales = step_scales(how, &last_bits);
 
