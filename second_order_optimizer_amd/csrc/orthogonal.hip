@@ -416,14 +416,14 @@ __device__ inline void sum_stages(const GemmProb& P, const Place& at, int s0, in
           for (int j = 0; j < NJ; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[cur][PLANES == 2 && x == 2][i], fb[cur][PLANES == 2 && x == 1][j],
                                                                acc[i][j], 0, 0, 0);
-      if (ks + 16 < BK) {
+      if (ks + 16 < BK && MFMAS >= READS) {
 #pragma unroll
         for (int u = 0; u < READS; ++u) {
           __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
           __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
         }
-        __builtin_amdgcn_sched_group_barrier(kSchedMfma, MFMAS - READS, 0);
-      } else {
+        __builtin_amdgcn_sched_group_barrier(kSchedMfma, MFMAS >= READS ? MFMAS - READS : 0, 0);
+      } else if (ks + 16 >= BK) {
         __builtin_amdgcn_sched_group_barrier(kSchedMfma, MFMAS, 0);
       }
     }
@@ -781,13 +781,16 @@ std::vector<StepScale> step_scales(const kfac_orthogonal_t& how, int* last) {
 
 using Half256 = Tile<1, 256, 256, 4, 2, 64, 2>;
 using Half128 = Tile<1, 128, 128, 2, 2, 64, 2>;
+using Half128Wide = Tile<1, 128, 128, 1, 2, 64, 3>;
 using Full256 = Tile<2, 256, 256, 4, 2, 32, 2>;
 using Full128 = Tile<2, 128, 128, 2, 2, 32, 2>;
+using Full128Wide = Tile<2, 128, 128, 1, 2, 32, 3>;
 
 // How a launch's tiles are cut: their size, and the workgroups that share their
 // stages (0: each takes a tile).
 struct Cut {
   int tile, shares;
+  bool wide;             // eight wavefronts a tile of 128, for at most a workgroup a compute unit
 };
 struct Product {
   int64_t tiles[2], units[2];      // of 128 and of 256
@@ -796,7 +799,7 @@ struct Product {
 // workgroup a compute unit (two, for tiles of 128, where there are that many), an
 // epilogue, and shares written and read again at 4 TB/s with a launch of their own.
 Cut cut_of(const Product& p, int planes, bool may256) {
-  Cut best{128, 0};
+  Cut best{128, 0, false};
   double least = 1e30;
   for (int big = may256 ? 1 : 0; big >= 0; --big) {
     const double tiles = static_cast<double>(p.tiles[big]), units = static_cast<double>(p.units[big]), stages = units / tiles;
@@ -807,13 +810,13 @@ Cut cut_of(const Product& p, int planes, bool may256) {
     };
     const double rounds = std::ceil(tiles / slots), end = big ? 30.0 : 12.0;
     const double whole = rounds * (stages * stage(std::min(tiles, static_cast<double>(slots))) + end);
-    if (whole < least) least = whole, best = {big ? 256 : 128, 0};
+    if (whole < least) least = whole, best = {big ? 256 : 128, 0, !big && tiles <= 256.0};
     const double bytes = big ? 524288.0 : 131072.0;          // a share's sums, written and read
     for (int g = 32; g <= slots; g += 32) {
       if (units < 2.0 * g || g < tiles * 0.5) continue;
       // (workgroups at different places of the contraction read no panels together)
       const double t = units / g * stage(0) * (1.0 + g / (big ? 256.0 : 350.0)) + (g + tiles) * bytes / 4e6 + 10.0 + end;
-      if (t < 0.95 * least) least = t, best = {big ? 256 : 128, g};
+      if (t < 0.95 * least) least = t, best = {big ? 256 : 128, g, !big && g <= 256};
     }
   }
   return best;
@@ -847,8 +850,10 @@ template <Kind KIND>
 kfac_status_t launch_products(std::vector<GemmProb>& probs, const std::vector<int>& batch, int planes, Cut cut, float* partial, hipStream_t st) {
   if (planes == 2)
     return cut.tile == 256 ? launch_tiles<Full256, KIND>(probs, batch, cut.shares, partial, st)
+           : cut.wide      ? launch_tiles<Full128Wide, KIND>(probs, batch, cut.shares, partial, st)
                            : launch_tiles<Full128, KIND>(probs, batch, cut.shares, partial, st);
   return cut.tile == 256 ? launch_tiles<Half256, KIND>(probs, batch, cut.shares, partial, st)
+         : cut.wide      ? launch_tiles<Half128Wide, KIND>(probs, batch, cut.shares, partial, st)
                          : launch_tiles<Half128, KIND>(probs, batch, cut.shares, partial, st);
 }
 
