@@ -22,6 +22,17 @@
 // matrix carries a power of two that keeps |value| <= 2^15: the norm bounds
 // every element, and the polynomial's maximum bounds the norm after each step.
 //
+// Pairs.  Of a long X two of three products grow with n.  With FULL, where those
+// weigh enough, two steps meet X in one: with P = a I + B of the first step, X's
+// next X X^T is P A P, B' comes of that, and
+//     X <- (a' I + B') P X = a a' X + (a' P + B' P - a a' I) X,
+// one product with X, one X X^T and five d x d ones (symmetric all, as the factors
+// are polynomials of A) in place of two, two and two; an odd step stays by itself.
+// In 22 bits that is as exact (2e-6 of the result where a step at a time is 1e-6,
+// both 2e-5 where eight directions make up nearly all of X); in 11 bits it would
+// double the error, so HALF takes a step at a time.  Eight layers of 1024 x 4096:
+// 2.51 -> 2.01 ms.
+//
 // Layout.  Planes are row-major, both sides padded with zeros to whole tiles,
 // which every product keeps at zero: no bounds checks outside the first and last
 // pass.
@@ -214,7 +225,7 @@ struct GemmProb {
   int32_t lda, ldb, ldo, ldot;      // c is laid out as o
   int32_t k, tm, tn, tiles, blk_begin;      // tiles of a matrix; the first of all
   int64_t unit_begin;                       // the first stage of all
-  float s_acc, s_c;           // result = s_acc P Q^T + s_c C
+  float s_acc, s_c, s_diag;   // result = s_acc P Q^T + s_c C + s_diag I (s_diag: FULL, kPoly)
   float *d_out, *d_in;        // HALF: the diagonal that the result leaves out, and the one that B left out,
   int32_t d_batch, d_cols;    // a value a row of C, or a column
   // last product: the update goes to y, or into w
@@ -276,7 +287,7 @@ __device__ inline GemmProb prob_regs(const GemmProb& p) {
   q.lda = arg_reg(p.lda), q.ldb = arg_reg(p.ldb), q.ldo = arg_reg(p.ldo), q.ldot = arg_reg(p.ldot);
   q.k = arg_reg(p.k), q.tm = arg_reg(p.tm), q.tn = arg_reg(p.tn), q.tiles = arg_reg(p.tiles);
   q.blk_begin = arg_reg(p.blk_begin), q.unit_begin = arg_reg(p.unit_begin);
-  q.s_acc = arg_reg(p.s_acc), q.s_c = arg_reg(p.s_c), q.d_out = arg_reg(p.d_out), q.d_in = arg_reg(p.d_in);
+  q.s_acc = arg_reg(p.s_acc), q.s_c = arg_reg(p.s_c), q.s_diag = arg_reg(p.s_diag), q.d_out = arg_reg(p.d_out), q.d_in = arg_reg(p.d_in);
   q.d_batch = arg_reg(p.d_batch), q.d_cols = arg_reg(p.d_cols);
   q.y = arg_reg(p.y), q.w = arg_reg(p.w), q.y_ld = arg_reg(p.y_ld), q.y_batch = arg_reg(p.y_batch);
   q.rows = arg_reg(p.rows), q.cols = arg_reg(p.cols), q.y_bf16 = arg_reg(p.y_bf16);
@@ -547,6 +558,11 @@ __device__ inline void finish(const GemmProb& P, const Place& at, int wid, f32x1
             if (at_e == e) d = v[e], v[e] = 0.f;
           if (at_e >= 0 && at_e < 8) P.d_out[static_cast<int64_t>(mat) * P.d_batch + row] = d;
         }
+        if (KIND == kPoly && PLANES == 2 && below(i) == 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (row - col == e) v[e] += P.s_diag;
+        }
         f16x8 hi, lo;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -732,7 +748,7 @@ Shape shape_of(const OrthTask& t) {
 }
 
 struct Region {
-  size_t part, same[2], turned[2], a, b, diag;      // X as x lies and turned; what B X reads is not what it writes
+  size_t part, same[2], turned[2], a, b, s, diag;      // X as x lies and turned; what B X reads is not what it writes
 };
 size_t plan(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how, std::vector<Region>* out) {
   const int planes = how.products == KFAC_PRODUCTS_FULL ? 2 : 1;
@@ -744,7 +760,7 @@ size_t plan(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how, st
   };
   for (const OrthTask& t : tasks) {
     const Shape s = shape_of(t);
-    Region r;
+    Region r{};
     const size_t batch = static_cast<size_t>(t.batch);
     r.part = take(sizeof(double) * kNormBlocks * batch);
     const size_t both = 2 * 2 * batch * s.x_plane, some = 2 * planes * batch * s.x_plane;
@@ -754,6 +770,7 @@ size_t plan(const std::vector<OrthTask>& tasks, const kfac_orthogonal_t& how, st
     r.turned[1] = s.tall ? r.turned[0] : take(some);
     r.a = take(2 * planes * batch * s.a_plane);
     r.b = take(2 * planes * batch * s.a_plane);
+    if (planes == 2) r.s = take(2 * planes * batch * s.a_plane);
     r.diag = take(sizeof(float) * batch * s.dp);
     if (out) out->push_back(r);
   }
@@ -766,13 +783,14 @@ int bits_for(double bound) { return 15 - static_cast<int>(std::ceil(std::log2(st
 // Norm bounds after each step, over all singular values that the last one allows.
 struct StepScale {
   int x, a, b;           // powers of two of X, A, B in this step
+  double rho, pb;        // bounds of |X| and |B|
 };
 std::vector<StepScale> step_scales(const kfac_orthogonal_t& how, int* last) {
   std::vector<StepScale> out;
   double rho = 1.0;
   for (int s = 0; s < how.steps; ++s) {
     const PolyBound p = poly_of(how.coefs + 3 * s, rho);
-    out.push_back({bits_for(rho), bits_for(rho * rho), bits_for(p.b)});
+    out.push_back({bits_for(rho), bits_for(rho * rho), bits_for(p.b), rho, p.b});
     rho = p.next;
   }
   *last = bits_for(rho);
@@ -791,6 +809,7 @@ using Full128Wide = Tile<2, 128, 128, 1, 2, 32, 3>;
 struct Cut {
   int tile, shares;
   bool wide;             // eight wavefronts a tile of 128, for at most a workgroup a compute unit
+  double time;           // what it should take, us
 };
 struct Product {
   int64_t tiles[2], units[2];      // of 128 and of 256
@@ -799,7 +818,7 @@ struct Product {
 // workgroup a compute unit (two, for tiles of 128, where there are that many), an
 // epilogue, and shares written and read again at 4 TB/s with a launch of their own.
 Cut cut_of(const Product& p, int planes, bool may256) {
-  Cut best{128, 0, false};
+  Cut best{128, 0, false, 0.0};
   double least = 1e30;
   for (int big = may256 ? 1 : 0; big >= 0; --big) {
     const double tiles = static_cast<double>(p.tiles[big]), units = static_cast<double>(p.units[big]), stages = units / tiles;
@@ -810,13 +829,13 @@ Cut cut_of(const Product& p, int planes, bool may256) {
     };
     const double rounds = std::ceil(tiles / slots), end = big ? 30.0 : 12.0;
     const double whole = rounds * (stages * stage(std::min(tiles, static_cast<double>(slots))) + end);
-    if (whole < least) least = whole, best = {big ? 256 : 128, 0, !big && tiles <= 256.0};
+    if (whole < least) least = whole, best = {big ? 256 : 128, 0, !big && tiles <= 256.0, whole};
     const double bytes = big ? 524288.0 : 131072.0;          // a share's sums, written and read
     for (int g = 32; g <= slots; g += 32) {
       if (units < 2.0 * g || g < tiles * 0.5) continue;
       // (workgroups at different places of the contraction read no panels together)
       const double t = units / g * stage(0) * (1.0 + g / (big ? 256.0 : 350.0)) + (g + tiles) * bytes / 4e6 + 10.0 + end;
-      if (t < 0.95 * least) least = t, best = {big ? 256 : 128, g, !big && g <= 256};
+      if (t < 0.95 * least) least = t, best = {big ? 256 : 128, g, !big && g <= 256, t};
     }
   }
   return best;
@@ -861,6 +880,7 @@ kfac_status_t launch_products(std::vector<GemmProb>& probs, const std::vector<in
 struct Group {
   std::vector<size_t> tasks;
   Cut gram, poly, next;
+  bool pairs;            // two steps a product with X
 };
 std::vector<Group> groups_of(const std::vector<OrthTask>& tasks, int planes) {
   std::vector<Group> out;
@@ -883,6 +903,8 @@ std::vector<Group> groups_of(const std::vector<OrthTask>& tasks, int planes) {
       g.gram = cut_of(a, planes, tile == 256);
       g.poly = cut_of(b, planes, tile == 256);
       g.next = cut_of(x, planes, tile == 256);
+      // three more d x d products against an X X^T and a product with X
+      g.pairs = planes == 2 && g.gram.time + g.next.time > 3.3 * g.poly.time;
       out.push_back(g);
       g = Group{};
     };
@@ -973,95 +995,123 @@ kfac_status_t launch_orthogonal(const std::vector<OrthTask>& all, const kfac_ort
   }
 
   auto two = [](int e) { return std::ldexp(1.f, e); };
-  for (const Group& g : groups_of(tasks, planes))
-  for (int k = 0; k < how.steps; ++k) {
-    const float a = how.coefs[3 * k], b = how.coefs[3 * k + 1], c = how.coefs[3 * k + 2];
-    const StepScale& sc = scales[k];
-    const bool last = k + 1 == how.steps;
-    const int xb = last ? 0 : scales[k + 1].x;         // the last X is written as it is
-    std::vector<GemmProb> pa, pb, px;
-    std::vector<int> batch;
-    for (size_t i : g.tasks) {
-      const OrthTask& t = tasks[i];
-      batch.push_back(t.batch);
-      const Shape s = shape_of(t);
-      const Region& r = regions[i];
-      // X as x lies, [rows_p, cols_p], and turned; the one with d rows and n columns
-      f16* same = reinterpret_cast<f16*>(ws + r.same[k & 1]);
-      f16* turned = reinterpret_cast<f16*>(ws + r.turned[k & 1]);
-      f16* A = reinterpret_cast<f16*>(ws + r.a);
-      f16* B = reinterpret_cast<f16*>(ws + r.b);
-      const int64_t a_plane2 = planes == 2 ? s.a_plane : 0;
-      GemmProb p{};
-      p.a = p.b = s.tall ? turned : same;
-      p.a_plane = p.b_plane = s.x_plane;
-      p.a_batch = p.b_batch = s.x_plane * (s.tall ? planes : 2);
-      p.lda = p.ldb = s.np;
-      p.o = p.ot = A;
-      p.o_plane = p.ot_plane = a_plane2;
-      p.o_batch = p.ot_batch = s.a_plane * planes;
-      p.ldo = p.ldot = s.dp;
-      p.k = s.np;
-      p.tm = p.tn = s.dp;
-      p.s_acc = two(sc.a - 2 * sc.x);
-      pa.push_back(p);
-      p.a = p.b = A;
-      p.a_plane = p.b_plane = s.a_plane;
-      p.a_batch = p.b_batch = s.a_plane * planes;
-      p.lda = p.ldb = s.dp;
-      p.c = A;
-      p.c_plane = a_plane2;
-      p.c_batch = s.a_plane * planes;
-      p.o = p.ot = B;
-      p.d_out = reinterpret_cast<float*>(ws + r.diag);
-      p.d_batch = s.dp;
-      p.k = s.dp;
-      p.s_acc = c * two(sc.b - 2 * sc.a);
-      p.s_c = b * two(sc.b - sc.a);
-      pb.push_back(p);
-      // B X, or X^T B where x is taller than wide
-      const f16* xt = s.tall ? same : turned;
-      const int64_t xt_batch = s.x_plane * (s.tall ? 2 : planes);
-      p.a = s.tall ? xt : B;
-      p.b = s.tall ? B : xt;
-      p.a_plane = s.tall ? s.x_plane : s.a_plane;
-      p.b_plane = s.tall ? s.a_plane : s.x_plane;
-      p.a_batch = s.tall ? xt_batch : s.a_plane * planes;
-      p.b_batch = s.tall ? s.a_plane * planes : xt_batch;
-      p.d_in = p.d_out;
-      p.d_cols = s.tall;
-      p.d_out = nullptr;
-      p.c = same;
-      p.o = reinterpret_cast<f16*>(ws + r.same[(k + 1) & 1]);
-      p.c_plane = p.o_plane = s.x_plane;
-      p.c_batch = p.o_batch = s.x_plane * 2;
-      p.ldo = s.tall ? s.dp : s.np;
-      p.ot = reinterpret_cast<f16*>(ws + r.turned[(k + 1) & 1]);
-      p.ot_plane = s.x_plane;
-      p.ot_batch = s.x_plane * planes;
-      p.ldot = s.tall ? s.np : s.dp;
-      p.tm = s.tall ? s.np : s.dp;
-      p.tn = s.tall ? s.dp : s.np;
-      p.s_acc = two(xb - sc.b - sc.x);
-      p.s_c = a * two(xb - sc.x);
-      p.y = t.y;
-      p.w = t.w;
-      p.y_ld = t.w ? t.cols : t.y_ld;
-      p.y_batch = t.w ? 0 : t.y_stride;
-      p.rows = t.rows;
-      p.cols = t.cols;
-      p.y_bf16 = t.dtype == KFAC_BF16;
-      p.decay = 1.f - step.lr * step.weight_decay;
-      p.factor = t.factor;
-      px.push_back(p);
+  for (const Group& g : groups_of(tasks, planes)) {
+    int from = 0;                        // where X is: of the two, for products with X so far
+    for (int k = 0, n; k < how.steps; k += n, from ^= 1) {
+      n = g.pairs && k + 1 < how.steps ? 2 : 1;
+      const float *c1 = how.coefs + 3 * k, *c2 = c1 + 3;
+      const StepScale& sc = scales[k];
+      const bool last = k + n == how.steps;
+      const int xb = last ? 0 : scales[k + n].x;         // the last X is written as it is
+      std::vector<GemmProb> pa, px;
+      std::vector<std::vector<GemmProb>> polys(n == 2 ? 5 : 1);
+      std::vector<int> batch;
+      for (size_t i : g.tasks) {
+        const OrthTask& t = tasks[i];
+        batch.push_back(t.batch);
+        const Shape s = shape_of(t);
+        const Region& r = regions[i];
+        // X as x lies, [rows_p, cols_p], and turned; the one with d rows and n columns
+        f16* same = reinterpret_cast<f16*>(ws + r.same[from]);
+        f16* turned = reinterpret_cast<f16*>(ws + r.turned[from]);
+        f16 *A = reinterpret_cast<f16*>(ws + r.a), *B = reinterpret_cast<f16*>(ws + r.b), *S = reinterpret_cast<f16*>(ws + r.s);
+        const int64_t a_plane2 = planes == 2 ? s.a_plane : 0;
+        GemmProb p{};
+        p.a = p.b = s.tall ? turned : same;
+        p.a_plane = p.b_plane = s.x_plane;
+        p.a_batch = p.b_batch = s.x_plane * (s.tall ? planes : 2);
+        p.lda = p.ldb = s.np;
+        p.o = p.ot = A;
+        p.o_plane = p.ot_plane = a_plane2;
+        p.o_batch = p.ot_batch = s.a_plane * planes;
+        p.ldo = p.ldot = s.dp;
+        p.k = s.np;
+        p.tm = p.tn = s.dp;
+        p.s_acc = two(sc.a - 2 * sc.x);
+        pa.push_back(p);
+        // among d x d matrices: out = by s_acc, s_c and s_diag from left right and c
+        p.a_plane = p.b_plane = s.a_plane;
+        p.a_batch = p.b_batch = s.a_plane * planes;
+        p.lda = p.ldb = s.dp;
+        p.c_plane = a_plane2;
+        p.c_batch = s.a_plane * planes;
+        p.d_out = reinterpret_cast<float*>(ws + r.diag);
+        p.d_batch = s.dp;
+        p.k = s.dp;
+        auto poly = [&](int which, f16* out, const f16* left, const f16* right, const f16* c, float s_acc, float s_c, float s_diag) {
+          p.o = p.ot = out;
+          p.a = left;
+          p.b = right;
+          p.c = c;
+          p.s_acc = s_acc;
+          p.s_c = s_c;
+          p.s_diag = s_diag;
+          polys[which].push_back(p);
+        };
+        float a = c1[0];                   // X <- a X + M X
+        f16* M = B;
+        int m_bits = sc.b;
+        if (n == 1) {
+          poly(0, B, A, A, A, c1[2] * two(sc.b - 2 * sc.a), c1[1] * two(sc.b - sc.a), 0.f);
+        } else {
+          const StepScale& next = scales[k + 1];
+          const int pbits = bits_for(std::fabs(c1[0]) + sc.pb), sbits = bits_for(sc.rho * next.rho);
+          // (the last term: what P's rounding leaves of a I - a I)
+          m_bits = bits_for(std::fabs(c1[0]) * next.pb + std::fabs(c2[0]) * sc.pb + sc.pb * next.pb +
+                            std::ldexp(std::fabs(c2[0]) * (std::fabs(c1[0]) + sc.pb), -18));
+          a = c1[0] * c2[0];
+          M = A;
+          poly(0, B, A, A, A, c1[2] * two(pbits - 2 * sc.a), c1[1] * two(pbits - sc.a), c1[0] * two(pbits));          // P
+          poly(1, S, B, A, A, two(sbits - pbits - sc.a), 0.f, 0.f);                                                   // P A
+          poly(2, A, S, B, B, two(next.a - sbits - pbits), 0.f, 0.f);                                                 // P A P
+          poly(3, S, A, A, A, c2[2] * two(next.b - 2 * next.a), c2[1] * two(next.b - next.a), 0.f);                   // B of it
+          poly(4, A, S, B, B, two(m_bits - next.b - pbits), c2[0] * two(m_bits - pbits), -a * two(m_bits));
+        }
+        // M X, or X^T M where x is taller than wide
+        const f16* xt = s.tall ? same : turned;
+        const int64_t xt_batch = s.x_plane * (s.tall ? 2 : planes);
+        p.a = s.tall ? xt : M;
+        p.b = s.tall ? M : xt;
+        p.a_plane = s.tall ? s.x_plane : s.a_plane;
+        p.b_plane = s.tall ? s.a_plane : s.x_plane;
+        p.a_batch = s.tall ? xt_batch : s.a_plane * planes;
+        p.b_batch = s.tall ? s.a_plane * planes : xt_batch;
+        p.d_in = p.d_out;
+        p.d_cols = s.tall;
+        p.d_out = nullptr;
+        p.c = same;
+        p.o = reinterpret_cast<f16*>(ws + r.same[from ^ 1]);
+        p.c_plane = p.o_plane = s.x_plane;
+        p.c_batch = p.o_batch = s.x_plane * 2;
+        p.ldo = s.tall ? s.dp : s.np;
+        p.ot = reinterpret_cast<f16*>(ws + r.turned[from ^ 1]);
+        p.ot_plane = s.x_plane;
+        p.ot_batch = s.x_plane * planes;
+        p.ldot = s.tall ? s.np : s.dp;
+        p.tm = s.tall ? s.np : s.dp;
+        p.tn = s.tall ? s.dp : s.np;
+        p.s_acc = two(xb - m_bits - sc.x);
+        p.s_c = a * two(xb - sc.x);
+        p.y = t.y;
+        p.w = t.w;
+        p.y_ld = t.w ? t.cols : t.y_ld;
+        p.y_batch = t.w ? 0 : t.y_stride;
+        p.rows = t.rows;
+        p.cols = t.cols;
+        p.y_bf16 = t.dtype == KFAC_BF16;
+        p.decay = 1.f - step.lr * step.weight_decay;
+        p.factor = t.factor;
+        px.push_back(p);
+      }
+      kfac_status_t r = launch_products<kGram>(pa, batch, planes, g.gram, partial, st);
+      for (std::vector<GemmProb>& q : polys)
+        if (r == KFAC_OK) r = launch_products<kPoly>(q, batch, planes, g.poly, partial, st);
+      if (r == KFAC_OK)
+        r = !last ? launch_products<kNext>(px, batch, planes, g.next, partial, st)
+            : px[0].w ? launch_products<kWeight>(px, batch, planes, g.next, partial, st)
+                      : launch_products<kLast>(px, batch, planes, g.next, partial, st);
+      if (r != KFAC_OK) return r;
     }
-    kfac_status_t r = launch_products<kGram>(pa, batch, planes, g.gram, partial, st);
-    if (r == KFAC_OK) r = launch_products<kPoly>(pb, batch, planes, g.poly, partial, st);
-    if (r == KFAC_OK)
-      r = !last ? launch_products<kNext>(px, batch, planes, g.next, partial, st)
-          : px[0].w ? launch_products<kWeight>(px, batch, planes, g.next, partial, st)
-                    : launch_products<kLast>(px, batch, planes, g.next, partial, st);
-    if (r != KFAC_OK) return r;
   }
   return KFAC_OK;
 }

@@ -96,6 +96,23 @@ def test_steps_and_coefficients(M):
     assert e.value.status == 5
 
 
+@pytest.mark.parametrize("rows,cols,steps", [(512, 6000, 5), (12000, 700, 4), (1024, 8192, 1), (1000, 9001, 2), (1300, 7000, 3), (1024, 8192, 5)])
+def test_two_steps_a_product(M, rows, cols, steps):
+    """Long matrices in float32, for which pairs of steps meet X in one product; an odd step out is by itself."""
+    x, xd = draw(np.random.default_rng(cols), rows, cols)
+    op = M.Orthogonal(rows, cols, dtype="f32", steps=steps)
+    got = op.run(x)
+    print(rows, cols, steps, check(got, xd, "f32", "full", steps=steps))
+    assert op.flags() == 0 and torch.equal(got, op.run(x))
+
+
+@pytest.mark.parametrize("coefs", [((1.0, 0.0, 0.0),) * 2, ((2.0, -1.5, 0.5), (1.5, -0.5, 0.0)), ((0.0, 0.0, 0.0), (3.0, -2.0, 0.5)),
+                                   ((3.0, -2.5, 0.5), (0.0, 0.0, 0.0)), ((-1.0, 0.0, 2.0), (0.5, 0.25, -1.0))])
+def test_two_steps_of_any_coefficients(M, coefs):
+    x, xd = draw(np.random.default_rng(5), 700, 12000)
+    check(M.Orthogonal(700, 12000, dtype="f32", steps=2, coefs=coefs).run(x), xd, "f32", "full", coefs=coefs, steps=2)
+
+
 def test_values_that_are_far_apart(M):
     """Tiny and huge matrices, zeros, one entry, one huge row: the norm is 64-bit and the scale is the matrix's."""
     rng = np.random.default_rng(5)
