@@ -686,12 +686,17 @@ __global__ void __launch_bounds__(C::THREADS) orth_gemm_kernel(GemmBatch batch) 
   }
 }
 
-// A wavefront's part of a tile whose stages were shared: the shares in order.
+// 32 rows of a wavefront's part of a tile whose stages were shared: the shares in
+// order.  (A whole part a wavefront, 64 rows or 128, took twice as long: 21 tiles
+// of 20 shares 27 us, here 11.)
 template <typename C, Kind KIND>
 __global__ void __launch_bounds__(64) orth_join_kernel(GemmBatch batch) {
   constexpr bool SYM = KIND == kGram || KIND == kPoly;
+  using J = Tile<C::PLANES, C::BM, C::BN, 1, C::NJ, C::BK, C::SLOTS>;
+  static_assert(J::WN == C::WN);
   __shared__ __attribute__((aligned(16))) float mine[kMine];
-  const int lane = threadIdx.x, wid = blockIdx.x % C::WAVES, tile = blockIdx.x / C::WAVES;
+  const int lane = threadIdx.x, part = blockIdx.x % J::WAVES, tile = blockIdx.x / J::WAVES;
+  const int i = part / C::WN % C::MI, wid = part / C::WN / C::MI * C::WN + part % C::WN;
   int pi = 0;
   while (pi + 1 < batch.n && batch.p[pi + 1].blk_begin <= tile) ++pi;
   const GemmProb P = prob_regs(batch.p[pi]);
@@ -699,29 +704,27 @@ __global__ void __launch_bounds__(64) orth_join_kernel(GemmBatch batch) {
   const int64_t begin = P.unit_begin + static_cast<int64_t>(tile - P.blk_begin) * stages;
   const int w0 = share_of(batch, begin), w1 = share_of(batch, begin + stages - 1);
   if (w0 == w1) return;                      // one workgroup had all of it
-  f32x16 acc[C::MI][C::NJ];
+  f32x16 acc[1][C::NJ];
 #pragma unroll
-  for (int i = 0; i < C::MI; ++i)
+  for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[0][j][r] = 0.f;
+  const int begun = share_begin(batch, w0) < begin;        // the first share's workgroup had begun with another tile
+#pragma unroll 4
+  for (int w = w0; w <= w1; ++w) {
+    const int second = w == w0 && begun;
+    const f32x4* from = reinterpret_cast<const f32x4*>(batch.partial + (2 * static_cast<int64_t>(w) + second) * (C::BM * C::BN)) +
+                        (wid * C::MI + i) * (C::NJ * 4 * 64) + lane;
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  for (int w = w0; w <= w1; ++w) {
-    const int second = w == w0 && share_begin(batch, w) < begin;
-    const f32x4* from = reinterpret_cast<const f32x4*>(batch.partial + (2 * static_cast<int64_t>(w) + second) * (C::BM * C::BN)) +
-                        wid * (C::MI * C::NJ * 4 * 64) + lane;
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 x = from[(j * 4 + q) * 64];
 #pragma unroll
-    for (int i = 0; i < C::MI; ++i)
-#pragma unroll
-      for (int j = 0; j < C::NJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4 x = from[((i * C::NJ + j) * 4 + q) * 64];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += x[e];
-        }
+        for (int e = 0; e < 4; ++e) acc[0][j][4 * q + e] += x[e];
+      }
   }
-  finish<C, KIND>(P, place_of_tile<SYM>(P, tile - P.blk_begin), wid, acc, mine);
+  finish<J, KIND>(P, place_of_tile<SYM>(P, tile - P.blk_begin), part, acc, mine);
 }
 
 // -- plan ----------------------------------------------------------------------
@@ -861,7 +864,7 @@ kfac_status_t launch_tiles(std::vector<GemmProb>& probs, const std::vector<int>&
   b.partial = partial;
   hipLaunchKernelGGL((orth_gemm_kernel<C, KIND>), dim3(static_cast<uint32_t>(shares ? shares : tiles)), dim3(C::THREADS), 0, st, b);
   if (shares)
-    hipLaunchKernelGGL((orth_join_kernel<C, KIND>), dim3(static_cast<uint32_t>(tiles * C::WAVES)), dim3(64), 0, st, b);
+    hipLaunchKernelGGL((orth_join_kernel<C, KIND>), dim3(static_cast<uint32_t>(tiles * (C::WAVES * C::MI))), dim3(64), 0, st, b);
   return hipGetLastError() == hipSuccess ? KFAC_OK : KFAC_ERR_HIP;
 }
 
