@@ -40,7 +40,8 @@ extern "C" {
  *   HALF  11 bits (IEEE half, scaled): O within 1e-3 of 64 bits (2-norm,
  *         relative; bfloat16's own rounding is 1.7e-3)
  *   FULL  22 bits (two halves, three products each): within 5e-6, as float32
- *         products are */
+ *         products are (2e-5 where a few directions make up nearly all of x)
+ * Matrices with a side of at most 64 take neither: they are iterated in 64 bits. */
 enum { KFAC_PRODUCTS_HALF = 0, KFAC_PRODUCTS_FULL = 1 };
 /* kfac_orthogonal_t.scale: the factor s of a layer's step, W [d_out, d_in]
  *   NONE 1, ASPECT sqrt(max(1, d_out / d_in)), RMS 0.2 sqrt(max(d_out, d_in)) */

@@ -44,9 +44,9 @@ enum { KFAC_TOK_SAMPLE = 0, KFAC_TOK_EMBEDDING = 1 };
  *     n_m   those with w >= min_p.
  * The token is the first column, by number, at which the running sum of the
  * kept w exceeds u times their whole sum.  T = 0 (any T below 1e-6) keeps the
- * first of the order alone; a T above 1e30 counts as 1e30.  logp is the token's log-probability in the whole
- * row, (x[token] - M) / T - log sum w (at T = 0 that of T = 1): what
- * kfac_token_logp gives at logit_scale = 1 / T.  Columns of minus infinity are
+ * first of the order alone; a T above 1e30 counts as 1e30.  logp is the token's
+ * log-probability in the whole row, (x[token] - M) / T - log sum w (at T = 0 that
+ * of T = 1): what kfac_token_logp gives at logit_scale = 1 / T.  Columns of minus infinity are
  * never kept; a row of nothing else has token -1, logp 0 and kept 0.
  *
  * A row with a NaN or plus infinity among its logits raises
@@ -73,7 +73,7 @@ typedef struct kfac_sample {
   double top_p;               /* 0 .. 1 */
   double min_p;               /* 0 .. 1 */
   int32_t top_k;              /* >= 0 */
-  int32_t vocab;              /* 1 .. 2^20 */
+  int32_t vocab;              /* 1 .. 2^20 - 1 */
   int32_t dtype;              /* KFAC_F32 | KFAC_BF16 */
   int32_t reserved;           /* must be 0 */
 } kfac_sample_t;

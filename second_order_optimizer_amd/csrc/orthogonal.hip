@@ -18,9 +18,11 @@
 // (where the singular values have come near 1 it is most of B), and so are X's
 // low halves, for the term a X: where a few strong directions make up most of X,
 // its rounding to 11 bits is large against all the others, which that term
-// carries; as operands of the products, where B hardly has them yet, 11 bits do.  bfloat16 outputs take HALF, float32 ones FULL.  Each
-// matrix carries a power of two that keeps |value| <= 2^15: the norm bounds
-// every element, and the polynomial's maximum bounds the norm after each step.
+// carries; as operands of the products, where B hardly has them yet, 11 bits do.
+// (Both together: 1.5e-3 -> 5e-4 of the result.)  bfloat16 outputs take HALF,
+// float32 ones FULL.  Each matrix carries a power of two that keeps |value| <= 2^15:
+// the norm bounds every element, and the polynomial's maximum bounds the norm after
+// each step.
 //
 // Pairs.  Of a long X two of three products grow with n.  With FULL, where those
 // weigh enough, two steps meet X in one: with P = a I + B of the first step, X's

@@ -28,8 +28,8 @@
 // only the log-probability's sum over columns that are not kept takes the
 // hardware's exp, 2^-22 off, and the first histograms, which decide nothing.  Those
 // are each thread's own, 32 words of LDS 4 NT bytes apart: an LDS atomic on float32
-// took 190 cycles a wavefront (100257 columns: 126 us), a read, an addition and a
-// write take ... .
+// took 190 cycles of a compute unit a wavefront (1023 rows of 100257 columns: 126 us),
+// a read, an addition and a write take 18.
 #include "tokens.h"
 
 #include <cmath>

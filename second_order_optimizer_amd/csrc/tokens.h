@@ -7,7 +7,7 @@
 
 namespace kfac {
 
-constexpr int32_t kSampleMaxVocab = 1 << 20;
+constexpr int32_t kSampleMaxVocab = (1 << 20) - 1;      // weights of up to 2^44 are added in 64 bits
 // one launch covers 2^32 - 1 threads: 256 for 64 tokens of the table, and for 128 positions
 constexpr int32_t kEmbeddingMaxVocab = 1 << 29;
 constexpr int64_t kEmbeddingMaxTokens = 1 << 30;

@@ -123,8 +123,8 @@ class Sampler(_Operator):
         self._where = type(self).__name__
         if rows < 0 or vocab < 1:
             self._fail("rows must be at least 0 and vocab at least 1")
-        if vocab > 1 << 20:
-            self._fail("vocab must be at most 2^20", KFAC_ERR_UNSUPPORTED)
+        if vocab >= 1 << 20:
+            self._fail("vocab must be below 2^20", KFAC_ERR_UNSUPPORTED)
         if not 0.0 <= temperature < float("inf"):
             self._fail("temperature must be at least 0 and finite")
         if not 0 <= top_k < 1 << 31:

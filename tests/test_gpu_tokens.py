@@ -156,6 +156,22 @@ def test_sample_draws_the_distribution(T):
     assert np.abs(np.bincount(token.cpu().numpy(), minlength=37) - n * p).max() <= 1.01
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sample_of_the_most_equal_columns(T, dtype):
+    """2^20 - 1 columns of the largest weight fill the 64 bits of their sum."""
+    vocab = (1 << 20) - 1
+    with pytest.raises(RuntimeError):
+        T.Sampler(3, vocab + 1, dtype)
+    x = torch.zeros(3, vocab, dtype=DT[dtype], device="cuda")
+    u = gpu(np.array([0.0, 0.61803, 1 - 2.0 ** -24], np.float32))
+    token, logp, kept = T.Sampler(3, vocab, dtype).run(x, u)
+    assert token.tolist() == [int(float(v) * vocab) for v in u.cpu().numpy().astype(np.float64)] and (kept == vocab).all()
+    near(logp, np.full(3, -np.log(vocab)), 2 * U * np.log(vocab))
+    token, _, kept = T.Sampler(3, vocab, dtype, top_p=0.7001).run(x, u)
+    n = int(np.ceil(0.7001 * vocab))
+    assert kept.tolist() == [n] * 3 and token.tolist() == [int(float(v) * n) for v in u.cpu().numpy().astype(np.float64)]
+
+
 def test_sample_of_no_rows_and_repeats(T):
     assert [v.numel() for v in T.Sampler(0, 9, "f32").run(torch.empty(0, 9, device="cuda"), torch.empty(0, device="cuda"))] == [0, 0, 0]
     x = torch.randn(64, 9000, device="cuda").bfloat16()
