@@ -3,7 +3,8 @@
 // With M the row's maximum, w[i] = exp((x[i] - M) / T), and columns ordered by
 // falling x, equal ones by rising number, the kept columns are a prefix of that
 // order: all columns above one border (x, number), which is what is looked for.
-// No row is sorted.  One workgroup a row, which is read once, into registers:
+// No row is sorted.  One workgroup a row (few long rows of which top_k keeps few:
+// sixteen, which list the k largest of a part each, and one that joins the lists):
 //
 //   top_k  The k-th largest of the threads' own maxima is at most the row's k-th
 //          largest: the columns from there on, hardly more than k, are put in a
@@ -43,6 +44,16 @@ constexpr double kLog2e = 1.4426950408889634;
 constexpr float kGreedy = 1e-6f;          // temperatures below this keep the maximum alone
 constexpr float kBinsPerOctave = 16.f;    // 1024 bins reach 2^-64 of the maximum's weight
 
+// What a workgroup finds in its part of a row that several take.
+constexpr int kSplitRows = 16, kSplitVocab = 65536, kSplitTopK = 64, kParts = 16;
+constexpr uint32_t kNoList = 0xFFFFFFFFu;
+struct Head {
+  double rest;             // sum of its columns' weights against its own maximum
+  float top;
+  uint32_t n;              // listed columns, or kNoList
+  uint64_t place[kSplitTopK];      // by rank
+};
+
 struct SampleArgs {
   const char* x;
   const float *u, *row_t, *row_p, *row_m;
@@ -54,6 +65,8 @@ struct SampleArgs {
   double t, p, m;
   int32_t k, vocab;
   uint32_t* flags;
+  Head* heads;       // [rows][parts], or none
+  int32_t parts;
 };
 
 // Columns above this one, and itself, in the order.
@@ -395,42 +408,13 @@ struct Drawn {
   double sum;            // of all w
 };
 
-// top_k, with top_p and min_p on what it keeps, and the draw, in a list of the
-// columns from the k-th largest of the threads' maxima (`own`) on.  False where the
-// list does not hold them.
-template <typename T, int NT, bool HELD>
-__device__ __forceinline__ bool draw_of_few(Shared<NT>& s, Listed* list, Row<T, NT, HELD>& row, const Scale& sc, float own, uint32_t k, double p, float low,
-                            float u, Drawn* out) {
-  constexpr int VE = Elem<T>::VE;
+// top_k, with top_p and min_p on what it keeps, and the draw, in a list of n <= NT
+// columns that holds the k largest (their places are in it); the whole row's sum is
+// in s.rest.
+template <int NT>
+__device__ __forceinline__ void draw_in_list(Shared<NT>& s, Listed* list, const Scale& sc, uint32_t n, uint32_t k, double p, float low, float u,
+                                             Drawn* out) {
   const int tid = threadIdx.x;
-  for (int b = tid; b < kBins; b += NT) s.count[b] = 0;
-  if (tid == 0) s.listed = 0;
-  __syncthreads();
-  if (own > -INFINITY) atomicAdd(&s.count[sc.bin(own)], 1u);
-  __syncthreads();
-  // (fewer than k threads have a column: all columns are listed)
-  const bool all = !find_bin<NT>(s, kBins, false, k, 0.0, true) || s.bin == kBins - 1;
-  const float reach = all ? 0.f : static_cast<float>(s.bin + 1);
-  const float cf = static_cast<float>(sc.c);
-  double rest = 0.0;
-  row.each([&](u32x4 v, int j) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float x = Elem<T>::get(v, i);
-      sum += __builtin_amdgcn_exp2f((x - sc.m) * cf);
-      if (((sc.m - x) * sc.bins < reach || all) && x > -INFINITY) {
-        const uint32_t at = atomicAdd(&s.listed, 1u);
-        if (at < NT) list[at].place = place_of(x, row.column(j, i));
-      }
-    }
-    rest += static_cast<double>(sum);
-  });
-  rest = wave_sum(rest);
-  if ((tid & (kWave - 1)) == 0) s.rest[tid / kWave] = rest;
-  __syncthreads();
-  const uint32_t n = s.listed;
-  if (n > NT) return false;
   uint64_t mine = 0, weight = 0;
   float x = 0.f;
   int32_t column = 0;
@@ -472,6 +456,50 @@ __device__ __forceinline__ bool draw_of_few(Shared<NT>& s, Listed* list, Row<T, 
     for (int w = 0; w < NT / kWave; ++w) sum += s.rest[w];
     *out = {column, static_cast<int32_t>(count), x, sum};
   }
+}
+
+// How far from the maximum, in bins, the k-th largest of the threads' `own` lies;
+// `all` where that is no bound (fewer than k have one, or it is in the last bin).
+template <int NT>
+__device__ __forceinline__ float reach_of(Shared<NT>& s, const Scale& sc, float own, uint32_t k, bool* all) {
+  for (int b = threadIdx.x; b < kBins; b += NT) s.count[b] = 0;
+  if (threadIdx.x == 0) s.listed = 0;
+  __syncthreads();
+  if (own > -INFINITY) atomicAdd(&s.count[sc.bin(own)], 1u);
+  __syncthreads();
+  *all = !find_bin<NT>(s, kBins, false, k, 0.0, true) || s.bin == kBins - 1;
+  return *all ? 0.f : static_cast<float>(s.bin + 1);
+}
+
+// The draw of a row of which top_k keeps few, in a list of the columns from the k-th
+// largest of the threads' maxima (`own`) on.  False where the list does not hold them.
+template <typename T, int NT, bool HELD>
+__device__ __forceinline__ bool draw_of_few(Shared<NT>& s, Listed* list, Row<T, NT, HELD>& row, const Scale& sc, float own, uint32_t k, double p, float low,
+                            float u, Drawn* out) {
+  constexpr int VE = Elem<T>::VE;
+  const int tid = threadIdx.x;
+  bool all;
+  const float reach = reach_of<NT>(s, sc, own, k, &all);
+  const float cf = static_cast<float>(sc.c);
+  double rest = 0.0;
+  row.each([&](u32x4 v, int j) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float x = Elem<T>::get(v, i);
+      sum += __builtin_amdgcn_exp2f((x - sc.m) * cf);
+      if (((sc.m - x) * sc.bins < reach || all) && x > -INFINITY) {
+        const uint32_t at = atomicAdd(&s.listed, 1u);
+        if (at < NT) list[at].place = place_of(x, row.column(j, i));
+      }
+    }
+    rest += static_cast<double>(sum);
+  });
+  rest = wave_sum(rest);
+  if ((tid & (kWave - 1)) == 0) s.rest[tid / kWave] = rest;
+  __syncthreads();
+  if (s.listed > NT) return false;
+  draw_in_list<NT>(s, list, sc, s.listed, k, p, low, u, out);
   return true;
 }
 
@@ -603,7 +631,169 @@ __device__ inline Border min_p_border(const Scale& sc, double m) {
   return {x, INT32_MAX};
 }
 
-template <typename T, int NT, bool HELD, bool CUT>
+// A row's settings.
+struct Settings {
+  float u;
+  double p, m, inv_t;
+  int32_t k;
+  bool valid;
+};
+__device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t r) {
+  Settings s;
+  s.u = a.u[r];
+  const float t = a.row_t ? a.row_t[r] : static_cast<float>(a.t);
+  s.p = a.row_p ? static_cast<double>(a.row_p[r]) : a.p;
+  s.m = a.row_m ? static_cast<double>(a.row_m[r]) : a.m;
+  s.k = a.row_k ? a.row_k[r] : a.k;
+  s.valid = s.u >= 0.f && s.u < 1.f && t >= 0.f && s.p == s.p && s.m == s.m;
+  s.inv_t = t < kGreedy ? 1.0 : 1.0 / fmin(a.row_t ? static_cast<double>(t) : a.t, 1e30);
+  if (t < kGreedy) s.k = 1;
+  return s;
+}
+__device__ __forceinline__ Scale scale_of(float top, double inv_t) {
+  Scale sc;
+  sc.m = top;
+  sc.c = kLog2e * inv_t;
+  sc.bins = static_cast<float>(sc.c) * kBinsPerOctave;
+  return sc;
+}
+
+// A part of a row of which top_k keeps few: its maximum, its sum, and its k largest.
+template <typename T>
+__global__ void __launch_bounds__(256) sample_head_kernel(SampleArgs a) {
+  constexpr int NT = 256, VE = Elem<T>::VE, NW = NT / kWave;
+  __shared__ Shared<NT> s;
+  __shared__ Listed list[NT];
+  const int64_t r = blockIdx.x / a.parts;
+  const int part = blockIdx.x % a.parts, tid = threadIdx.x;
+  Head& head = a.heads[blockIdx.x];
+  Row<T, NT, false> row;
+  row.fill(a.x + r * a.ldx, a.vocab);
+  const int per = (row.nvec + a.parts - 1) / a.parts, v0 = part * per, v1 = min(v0 + per, row.nvec);
+  const Settings set = settings_of(a, r);
+  float own = -INFINITY;
+  bool bad = false;
+#pragma unroll 4
+  for (int i = v0 + tid; i < v1; i += NT) {
+    const u32x4 v = row.load(i);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float x = Elem<T>::get(v, e);
+      bad |= !(x < INFINITY);
+      own = fmaxf(own, x);
+    }
+  }
+  float top = wave_max(own);
+  const bool any = __any(bad);
+  if (tid % kWave == 0) {
+    s.fmax[tid / kWave] = top;
+    s.fbad[tid / kWave] = any;
+  }
+  __syncthreads();
+  int nan = 0;
+  for (int w = 0; w < NW; ++w) {
+    top = fmaxf(top, s.fmax[w]);
+    nan |= s.fbad[w];
+  }
+  const bool few = set.valid && set.k > 0 && set.k <= kSplitTopK && !nan;
+  if (!few || top == -INFINITY) {
+    if (tid == 0) {
+      head.rest = 0.0;
+      head.top = top;
+      head.n = few ? 0 : kNoList;
+    }
+    return;
+  }
+  const Scale sc = scale_of(top, set.inv_t);
+  const float cf = static_cast<float>(sc.c);
+  bool all;
+  const float reach = reach_of<NT>(s, sc, own, static_cast<uint32_t>(set.k), &all);
+  double rest = 0.0;
+#pragma unroll 4
+  for (int i = v0 + tid; i < v1; i += NT) {
+    const u32x4 v = row.load(i);
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float x = Elem<T>::get(v, e);
+      sum += __builtin_amdgcn_exp2f((x - top) * cf);
+      if (((top - x) * sc.bins < reach || all) && x > -INFINITY) {
+        const uint32_t at = atomicAdd(&s.listed, 1u);
+        if (at < NT) list[at] = {place_of(x, i * VE + e), 0};
+      }
+    }
+    rest += static_cast<double>(sum);
+  }
+  rest = wave_sum(rest);
+  if (tid % kWave == 0) s.rest[tid / kWave] = rest;
+  __syncthreads();
+  const uint32_t n = s.listed;
+  if (n <= NT && tid < n) {
+    const uint64_t mine = list[tid].place;
+    uint32_t rank = 0;
+    uint64_t mass = 0;
+    before_in_list(list, n, mine, &rank, &mass);
+    if (rank < set.k) head.place[rank] = mine;
+  }
+  if (tid == 0) {
+    head.rest = (s.rest[0] + s.rest[1]) + (s.rest[2] + s.rest[3]);
+    head.top = top;
+    head.n = n <= NT ? min(n, static_cast<uint32_t>(set.k)) : kNoList;
+  }
+}
+
+// The lists of a row's parts, one column a thread: the row's maximum and sum in *top
+// and s.rest, the columns from the k-th largest on in `list`.  False where a part has
+// no list, or they are more than the threads.
+template <int NT>
+__device__ __forceinline__ bool join_heads(Shared<NT>& s, Listed* list, const Head* heads, int parts, const Settings& set, Scale* sc, uint32_t* n) {
+  // a lane a part: one read of memory in place of one after the other
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const uint32_t own_n = lane < parts ? heads[lane].n : 0;
+  const float top = wave_max(lane < parts ? heads[lane].top : -INFINITY);
+  if (__any(own_n == kNoList)) return false;
+  const uint32_t upto = wave_scan(own_n), count = __shfl(upto, kWave - 1);
+  if (count == 0 || count > NT) return false;
+  int from = 0;
+  uint32_t at = tid;
+  for (int g = 0; g + 1 < parts; ++g) {
+    const uint32_t end = __shfl(upto, g);
+    if (static_cast<uint32_t>(tid) >= end) {
+      from = g + 1;
+      at = tid - end;
+    }
+  }
+  *sc = scale_of(top, set.inv_t);
+  uint64_t place = 0;
+  float own = -INFINITY;
+  if (static_cast<uint32_t>(tid) < count) {
+    place = heads[from].place[at];
+    own = border_of(place).x;
+  }
+  bool all;
+  const float reach = reach_of<NT>(s, *sc, own, static_cast<uint32_t>(set.k), &all);
+  if (own > -INFINITY && ((top - own) * sc->bins < reach || all)) list[atomicAdd(&s.listed, 1u)].place = place;
+  if (tid < kWave) {
+    double rest = tid < parts ? heads[tid].rest : 0.0;
+    if (rest > 0.0) rest *= exp2((static_cast<double>(heads[tid].top) - static_cast<double>(top)) * sc->c);
+    rest = wave_sum(rest);
+    if (tid == 0) s.rest[0] = rest;
+  } else if (tid % kWave == 0) {
+    s.rest[tid / kWave] = 0.0;
+  }
+  __syncthreads();
+  *n = s.listed;
+  return true;
+}
+
+// The one thread that has the draw writes it.
+__device__ __forceinline__ void give(const SampleArgs& a, int64_t r, const Drawn& d, const Scale& sc, double inv_t) {
+  a.token[r] = d.token;
+  a.logp[r] = static_cast<float>((static_cast<double>(d.x) - static_cast<double>(sc.m)) * inv_t - log(d.sum));
+  a.kept[r] = d.kept;
+}
+
+template <typename T, int NT, bool HELD, bool CUT, bool SPLIT>
 __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   constexpr int VE = Elem<T>::VE, NW = NT / kWave;
   __shared__ Shared<NT> s;
@@ -618,14 +808,25 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   const int blocks = row.blocks();
   for (int j = tid; j < blocks; j += NT) block_mass[j] = 0;
 
-  // the row's settings
-  const float u = a.u[r];
-  float t = a.row_t ? a.row_t[r] : static_cast<float>(a.t);
-  double p = a.row_p ? static_cast<double>(a.row_p[r]) : a.p, m = a.row_m ? static_cast<double>(a.row_m[r]) : a.m;
-  int32_t k = a.row_k ? a.row_k[r] : a.k;
-  const bool valid = u >= 0.f && u < 1.f && t >= 0.f && p == p && m == m;
-  const double inv_t = t < kGreedy ? 1.0 : 1.0 / fmin(a.row_t ? static_cast<double>(t) : a.t, 1e30);
-  if (t < kGreedy) k = 1;
+  const Settings set = settings_of(a, r);
+  const float u = set.u;
+  const double p = set.p, m = set.m, inv_t = set.inv_t;
+  const int32_t k = set.k;
+  const bool valid = set.valid;
+  if constexpr (SPLIT) {
+    Scale sc;
+    uint32_t n;
+    if (join_heads<NT>(s, lists, a.heads + r * a.parts, a.parts, set, &sc, &n)) {
+      Border low{-INFINITY, -1};
+      if (m > 0.0) low = min_p_border(sc, fmin(m, 1.0));
+      Drawn d;
+      d.token = -1;
+      draw_in_list<NT>(s, lists, sc, n, static_cast<uint32_t>(k), k == 1 ? 1.0 : p, low.x, u, &d);
+      if (d.token >= 0) give(a, r, d, sc, inv_t);
+      return;
+    }
+    __syncthreads();
+  }
 
   // maximum, and whether every value is a number below infinity
   float top = -INFINITY;
@@ -663,10 +864,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
     return;
   }
 
-  Scale sc;
-  sc.m = top;
-  sc.c = kLog2e * inv_t;
-  sc.bins = static_cast<float>(sc.c) * kBinsPerOctave;
+  const Scale sc = scale_of(top, inv_t);
   Border border{-INFINITY, -1};
   bool summed = false;                       // block_mass and the count are there
   if constexpr (CUT) {
@@ -676,11 +874,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
       Drawn d;
       d.token = -1;
       if (draw_of_few<T, NT, HELD>(s, lists, row, sc, own, static_cast<uint32_t>(k), k == 1 ? 1.0 : p, low.x, u, &d)) {
-        if (d.token >= 0) {                  // the one thread that has it
-          a.token[r] = d.token;
-          a.logp[r] = static_cast<float>((static_cast<double>(d.x) - static_cast<double>(top)) * inv_t - log(d.sum));
-          a.kept[r] = d.kept;
-        }
+        if (d.token >= 0) give(a, r, d, sc, inv_t);
         return;
       }
       __syncthreads();
@@ -825,13 +1019,32 @@ kfac_status_t launch_typed(const SampleArgs& a, int64_t rows, hipStream_t st) {
   };
   // Wavefronts enough to fill the compute units with the rows that there are: a
   // workgroup of 1024 threads a unit, or two of 512, or (short rows) many of 256.
-  if (nvec <= 256) return go(sample_kernel<T, 256, true, CUT>, 256);
-  if (nvec <= 1024) return go(sample_kernel<T, 256, false, CUT>, 256);
-  if (rows > 256) return go(sample_kernel<T, 512, false, CUT>, 512);
-  return go(sample_kernel<T, 1024, false, CUT>, 1024);
+  if (nvec <= 256) return go(sample_kernel<T, 256, true, CUT, false>, 256);
+  if (nvec <= 1024) return go(sample_kernel<T, 256, false, CUT, false>, 256);
+  if (rows > 256) return go(sample_kernel<T, 512, false, CUT, false>, 512);
+  if constexpr (CUT) {
+    // few rows of which top_k keeps few: several workgroups a row find the largest
+    // columns of a part each
+    if (a.heads) {
+      hipLaunchKernelGGL(sample_head_kernel<T>, dim3(static_cast<uint32_t>(rows * a.parts)), dim3(256), 0, st, a);
+      return go(sample_kernel<T, 1024, false, CUT, true>, 1024);
+    }
+  }
+  return go(sample_kernel<T, 1024, false, CUT, false>, 1024);
 }
 
 }  // namespace
+
+// Workgroups of a row, where few long rows leave most compute units idle; 0: one alone.
+// (Two launches, a row as far as 131072 columns: 20 us against 30 alone; 8 rows of
+// 50000 21 against 22, one of 16384 13 against 11.)
+int sample_parts(int64_t rows, int32_t vocab) {
+  if (rows > kSplitRows || vocab < kSplitVocab) return 0;
+  return kParts;
+}
+size_t sample_workspace_bytes(int64_t rows, int32_t vocab) {
+  return kRegions + align_up(sizeof(Head) * static_cast<size_t>(rows) * sample_parts(rows, vocab), 256);
+}
 
 kfac_status_t launch_sample(const kfac_sample_t& s, char* ws, hipStream_t st) {
   if (s.rows == 0) return KFAC_OK;
@@ -852,6 +1065,10 @@ kfac_status_t launch_sample(const kfac_sample_t& s, char* ws, hipStream_t st) {
   a.k = s.top_k;
   a.vocab = s.vocab;
   a.flags = reinterpret_cast<uint32_t*>(ws);
+  a.parts = sample_parts(s.rows, s.vocab);
+  // (with top_k by row the rows without it take the longest, and the parts' launch is lost)
+  if (a.parts && !s.row_top_k && ((s.top_k > 0 && s.top_k <= kSplitTopK) || (!s.row_temperature && s.temperature < kGreedy)))
+    a.heads = reinterpret_cast<Head*>(ws + kRegions);
   const bool cut = s.row_temperature || s.row_top_k || s.row_top_p || s.row_min_p || s.top_k > 0 || s.top_p < 1.0 ||
                    s.min_p > 0.0 || s.temperature < kGreedy;
   if (s.dtype == KFAC_BF16) return cut ? launch_typed<__bf16, true>(a, s.rows, st) : launch_typed<__bf16, false>(a, s.rows, st);

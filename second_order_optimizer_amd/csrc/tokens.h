@@ -13,6 +13,7 @@ constexpr int32_t kEmbeddingMaxVocab = 1 << 29;
 constexpr int64_t kEmbeddingMaxTokens = 1 << 30;
 constexpr int32_t kEmbeddingMaxWidth = 1 << 24;
 
+size_t sample_workspace_bytes(int64_t rows, int32_t vocab);
 size_t embedding_workspace_bytes(int64_t tokens, int32_t vocab, int32_t width);
 
 kfac_status_t launch_sample(const kfac_sample_t& s, char* ws, hipStream_t st);

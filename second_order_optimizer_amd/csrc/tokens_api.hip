@@ -29,7 +29,7 @@ kfac_status_t kfac_token_workspace_size(int32_t op, int64_t rows, int32_t vocab,
   switch (op) {
     case KFAC_TOK_SAMPLE:
       if (vocab > kfac::kSampleMaxVocab) return KFAC_ERR_UNSUPPORTED;
-      *bytes = kfac::kRegions;
+      *bytes = kfac::sample_workspace_bytes(rows, vocab);
       return KFAC_OK;
     case KFAC_TOK_EMBEDDING:
       if (width < 1) return KFAC_ERR_ARG;
@@ -61,7 +61,7 @@ kfac_status_t kfac_sample_tokens(const kfac_sample_t* s, void* workspace, size_t
     p.need(s->kept, 4);
     if (p.s != KFAC_OK) return p.s;
   }
-  const kfac_status_t st = kfac::check_workspace(workspace, ws_bytes, kfac::kRegions);
+  const kfac_status_t st = kfac::check_workspace(workspace, ws_bytes, kfac::sample_workspace_bytes(s->rows, s->vocab));
   if (st != KFAC_OK) return st;
   return kfac::launch_sample(*s, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
 }

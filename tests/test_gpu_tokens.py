@@ -157,6 +157,43 @@ def test_sample_draws_the_distribution(T):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab", [(1, 65536), (2, 65541), (5, 80003), (16, 131072), (17, 65600), (3, 65535)])
+def test_sample_rows_in_parts(T, rows, vocab, dtype):
+    """Few rows, several workgroups each, and what sends a row back to one: settings of its own, ties, masks by the
+    part, values that are no numbers."""
+    rng = np.random.default_rng(vocab)
+    x, xd = matrix(rng, rows, vocab, dtype, pad=vocab % 4)
+    u = gpu(rng.random(rows).astype(np.float32))
+    for t, k, p, m in ((0.8, 50, 0.95, 0.0), (1.0, 64, 1.0, 0.0), (1.0, 65, 0.9, 0.0), (0.0, 0, 1.0, 0.0), (1.5, 1, 0.5, 0.1),
+                       (1.0, 7, 1.0, 0.3), (1e4, 33, 0.8, 0.0)):
+        op = T.Sampler(rows, vocab, dtype, temperature=t, top_k=k, top_p=p, min_p=m)
+        check(op.run(x, u), xd, u, t, k, p, m)
+        assert op.flags() == 0
+    t, p, m = (rng.choice(np.float32(v), rows).astype(np.float32) for v in
+               ([0.0, 0.5, 1.0, 2.0], [0.0, 0.3, 0.9, 1.0, 1.5], [-1.0, 0.0, 0.1, 1.0, 2.0]))
+    k = rng.choice([-3, 0, 1, 7, 40, 64, 65, 10 * vocab], rows).astype(np.int32)
+    op = T.Sampler(rows, vocab, dtype)
+    check(op.run(x, u, gpu(t), gpu(k), gpu(p), gpu(m)), xd, u, t, np.maximum(k, 0), np.clip(p, 0, 1), np.clip(m, 0, 1))
+    # all but a few columns masked: parts without any, and fewer left than top_k
+    y = torch.full_like(x, float("-inf"))
+    y[:, 3:vocab:vocab // 7] = x[:, 3:vocab:vocab // 7]
+    few = T.Sampler(rows, vocab, dtype, top_k=50, top_p=0.9)
+    check(few.run(y, u), wide(y), u, 1.0, 50, 0.9)
+    y[:, vocab // 2:] = float("-inf")
+    y[:, :9] = 2.0                                                     # equal ones, all in the first part
+    check(few.run(y, u), wide(y), u, 1.0, 50, 0.9)
+    y.fill_(1.0)                                                       # more equal ones than a list holds
+    token, _, kept = T.Sampler(rows, vocab, dtype, top_k=40).run(y, u)
+    assert kept.tolist() == [40] * rows and token.tolist() == [int(float(v) * 40) for v in u.cpu().numpy().astype(np.float64)]
+    y[0] = float("-inf")
+    y[-1, vocab - 1] = float("nan")
+    token, logp, kept = few.run(y, u)
+    bad = sorted({0, rows - 1})
+    assert (token[bad] == -1).all() and (logp[bad] == 0).all() and (kept[bad] == 0).all() and (token[1:-1] >= 0).all()
+    assert few.flags() != 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_sample_of_the_most_equal_columns(T, dtype):
     """2^20 - 1 columns of the largest weight fill the 64 bits of their sum."""
     vocab = (1 << 20) - 1
