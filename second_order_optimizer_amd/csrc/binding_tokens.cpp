@@ -79,6 +79,7 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[3] != Py_None) {
       y = c.tensor(a[3], "out");
       c.matrix(y, "out", e.tokens, e.width, &e.y_ld);
+      if (e.tokens > 0 && y.data_ptr() == e.table) c.refuse("out must not be table");
     }
     const bool given = y.defined();
     void* stream = c.enter();
@@ -102,6 +103,7 @@ PyObject* embedding_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[3] != Py_None) {
       grad = c.tensor(a[3], "grad");
       e.table = c.matrix_of(grad, "grad", e.table_dtype, e.vocab, e.width, &e.table_ld);
+      if (e.tokens > 0 && e.table == e.y) c.refuse("grad must not be dy");
     }
     const bool given = grad.defined();
     e.accumulate = a[4] == Py_True;
@@ -194,8 +196,10 @@ PyObject* orthogonal_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
           int64_t ld;
           L.grad_w = static_cast<const float*>(c.matrix(g, name, L.d_out, L.d_in, &ld));
           if (ld != L.d_in) c.refuse("grads must be contiguous");
+          if (L.grad_w == L.w || L.grad_w == L.mom_w) c.refuse("grads must not be weights or momenta");
         } else if (L.has_bias) {
           L.grad_b = static_cast<const float*>(c.vector(o, name, L.d_out, at::kFloat));
+          if (L.grad_b == L.b || L.grad_b == L.mom_b) c.refuse("bias_grads must not be biases or their momenta");
         } else if (o != Py_None) {
           c.refuse("bias_grads must be None for a layer without bias");
         }

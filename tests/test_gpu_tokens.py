@@ -174,6 +174,8 @@ def test_sample_rows_in_parts(T, rows, vocab, dtype):
     k = rng.choice([-3, 0, 1, 7, 40, 64, 65, 10 * vocab], rows).astype(np.int32)
     op = T.Sampler(rows, vocab, dtype)
     check(op.run(x, u, gpu(t), gpu(k), gpu(p), gpu(m)), xd, u, t, np.maximum(k, 0), np.clip(p, 0, 1), np.clip(m, 0, 1))
+    op = T.Sampler(rows, vocab, dtype, top_k=40)
+    check(op.run(x, u, gpu(t), None, gpu(p), gpu(m)), xd, u, t, 40, np.clip(p, 0, 1), np.clip(m, 0, 1))
     # all but a few columns masked: parts without any, and fewer left than top_k
     y = torch.full_like(x, float("-inf"))
     y[:, 3:vocab:vocab // 7] = x[:, 3:vocab:vocab // 7]

@@ -290,6 +290,10 @@ def test_run_refusals(lib):
     refused(D, e.backward, dy.bfloat16(), ids)
     refused(D, e.backward, dy, ids, grad=torch.zeros(8, 16))
     refused(A, e.backward, dy, ids, accumulate=True)
+    same = T.Embedding(8, 8, 16, dtype="f32", device="cpu")
+    square, eight = torch.zeros(8, 16), torch.zeros(8, dtype=torch.int64)
+    refused(A, same.run, square, eight, out=square)
+    refused(A, same.backward, square, eight, grad=square)
     o = M.Orthogonal(4, 8, batch=2, dtype="f32", device="cpu")
     y = torch.zeros(2, 4, 8)
     refused(U, o.run, y)
@@ -307,5 +311,7 @@ def test_run_refusals(lib):
     refused(A, s.run, [torch.zeros(8, 4).t()], [u])
     refused(D, s.run, [x.double()], [u])
     refused(A, M.OrthogonalStep([w], [m]).run, [x], [u])
+    for gw, gb in ((w, u), (m, u), (x, b), (x, bm)):
+        refused(A, s.run, [gw], [gb])
     with pytest.raises(TypeError):
         s.run([x], [u], lr="fast")
