@@ -836,6 +836,13 @@ Cut cut_of(const Product& p, int planes, bool may256) {
     const double whole = rounds * (stages * stage(std::min(tiles, static_cast<double>(slots))) + end);
     if (whole < least) least = whole, best = {big ? 256 : 128, 0, !big && tiles <= 256.0, whole};
     const double bytes = big ? 524288.0 : 131072.0;          // a share's sums, written and read
+    if (big && tiles > 0.5 * slots && tiles < slots) {
+      // Whole tiles would leave up to half of the compute units idle: thirds, of which
+      // two rounds run, at the same places of the contraction (X X^T of 4096 x 16384, 136
+      // tiles: 342 us whole, 282 and a join of 30 in thirds).
+      const double t = std::ceil(3.0 * tiles / slots) * stages / 3.0 * stage(0) + 4.0 * tiles * bytes / 4e6 + 10.0 + end;
+      if (t < 0.95 * least) least = t, best = {256, static_cast<int>(3 * p.tiles[big]), false, t};
+    }
     for (int g = 32; g <= slots; g += 32) {
       if (units < 2.0 * g || g < tiles * 0.5) continue;
       // (workgroups at different places of the contraction read no panels together)

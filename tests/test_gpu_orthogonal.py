@@ -106,6 +106,22 @@ def test_two_steps_a_product(M, rows, cols, steps):
     assert op.flags() == 0 and torch.equal(got, op.run(x))
 
 
+def test_thirds_of_tiles(M):
+    """A launch of 135 tiles of 256 with a long contraction, against 64-bit products on the GPU; the tolerance is
+    HALF's documented 1e-3 and the output's rounding."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(3, 2300, 20000, generator=gen, device="cuda").bfloat16()
+    got = M.Orthogonal(2300, 20000, batch=3).run(x)
+    for i in range(3):
+        z = x[i].double()
+        z /= z.norm() + 1e-7
+        a, b, c = np.asarray(O.COEFS, np.float32).astype(np.float64).tolist()
+        for _ in range(5):
+            g = z @ z.t().contiguous()
+            z = a * z + (b * g + c * g @ g) @ z
+        assert float((got[i].double() - z).norm()) <= (1e-3 + HALF["bf16"]) * float(z.norm()), i
+
+
 @pytest.mark.parametrize("coefs", [((1.0, 0.0, 0.0),) * 2, ((2.0, -1.5, 0.5), (1.5, -0.5, 0.0)), ((0.0, 0.0, 0.0), (3.0, -2.0, 0.5)),
                                    ((3.0, -2.5, 0.5), (0.0, 0.0, 0.0)), ((-1.0, 0.0, 2.0), (0.5, 0.25, -1.0))])
 def test_two_steps_of_any_coefficients(M, coefs):
