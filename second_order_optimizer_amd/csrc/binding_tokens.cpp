@@ -24,8 +24,9 @@ struct OrthogonalPlan {
 };
 struct StepPlan {
   Plan base;
-  kfac_layer_t* layers;        // kept by the operator, gradients set per call
-  PyObject* weights;           // lists of tensors that a step writes: weights, momenta, biases, bias momenta
+  kfac_layer_t* layers;        // kept by the operator, pointers set per call
+  PyObject* weights;           // list of the tensors that a step writes: weights, momenta, biases, bias momenta
+                               // (of the layers that have them)
   int64_t n;
   kfac_orthogonal_t how;
   kfac_hparams_t hp;
@@ -178,6 +179,22 @@ PyObject* orthogonal_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     float* to[3] = {&hp.lr, &hp.momentum, &hp.weight_decay};
     for (int i = 0; i < 3; ++i) *to[i] = static_cast<float>(PyFloat_AsDouble(a[3 + i]));
     if (PyErr_Occurred()) return nullptr;
+    // The tensors are the operator's own, but a program may have given them other memory (w.data = v): what they
+    // hold now is what is written.
+    Py_ssize_t next = 0;
+    auto kept = [&] { return PyList_GET_ITEM(plan->weights, next++); };
+    auto square = [&](const kfac_layer_t& L, const char* name) {
+      int64_t ld;
+      float* p = static_cast<float*>(c.matrix(THPVariable_Unpack(kept()), name, L.d_out, L.d_in, &ld));
+      if (ld != L.d_in) c.refuse(std::string(name) + " must be contiguous");
+      return p;
+    };
+    for (int64_t i = 0; i < plan->n; ++i) plan->layers[i].w = square(plan->layers[i], "a weight");
+    for (int64_t i = 0; i < plan->n; ++i) plan->layers[i].mom_w = square(plan->layers[i], "a momentum");
+    for (int64_t i = 0; i < plan->n; ++i)
+      if (plan->layers[i].has_bias) plan->layers[i].b = c.floats(kept(), "a bias", plan->layers[i].d_out);
+    for (int64_t i = 0; i < plan->n; ++i)
+      if (plan->layers[i].has_bias) plan->layers[i].mom_b = c.floats(kept(), "a bias momentum", plan->layers[i].d_out);
     for (int which = 0; which < 2; ++which) {
       const char* name = which ? "bias_grads" : "grads";
       PyObject* list = a[1 + which];
