@@ -7,6 +7,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
 
@@ -47,6 +48,15 @@ class Call {
   const at::Tensor& tensor(PyObject* o, const char* name) const {
     if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
     return THPVariable_Unpack(o);
+  }
+
+  // A tensor that a derivative may be taken through.  The backward passes are there, but no operator carries a
+  // forward-mode tangent on (without this its result would have none: a derivative of zero).
+  const at::Tensor& differentiable(PyObject* o, const char* name) const {
+    const at::Tensor& t = tensor(o, name);
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+      refuse(std::string(name) + " has a forward-mode tangent, and the operator no forward-mode derivative", KFAC_ERR_UNSUPPORTED);
+    return t;
   }
 
   bool placed(const at::Tensor& t) const {

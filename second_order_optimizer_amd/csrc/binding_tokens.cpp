@@ -69,7 +69,7 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const EmbeddingPlan* plan = plan_of<EmbeddingPlan>(a, n, 4);
     Call c(plan->base);
     kfac_embedding_t e = plan->e;
-    const at::Tensor& table = c.tensor(a[1], "table");
+    const at::Tensor& table = c.differentiable(a[1], "table");
     e.table = c.matrix_of(table, "table", e.table_dtype, e.vocab, e.width, &e.table_ld);
     e.ids = c.indices(a[2], "ids", e.tokens, -1, &e.id_type);
     if (c10::GradMode::is_enabled() && table.requires_grad()) {
@@ -78,7 +78,7 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     at::Tensor y;
     if (a[3] != Py_None) {
-      y = c.tensor(a[3], "out");
+      y = c.differentiable(a[3], "out");
       c.matrix(y, "out", e.tokens, e.width, &e.y_ld);
       if (e.tokens > 0 && y.data_ptr() == e.table) c.refuse("out must not be table");
     }
@@ -98,11 +98,11 @@ PyObject* embedding_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const EmbeddingPlan* plan = plan_of<EmbeddingPlan>(a, n, 5);
     Call c(plan->base);
     kfac_embedding_t e = plan->e;
-    e.y = c.matrix(c.tensor(a[1], "dy"), "dy", e.tokens, e.width, &e.y_ld);
+    e.y = c.matrix(c.differentiable(a[1], "dy"), "dy", e.tokens, e.width, &e.y_ld);
     e.ids = c.indices(a[2], "ids", e.tokens, -1, &e.id_type);
     at::Tensor grad;
     if (a[3] != Py_None) {
-      grad = c.tensor(a[3], "grad");
+      grad = c.differentiable(a[3], "grad");
       e.table = c.matrix_of(grad, "grad", e.table_dtype, e.vocab, e.width, &e.table_ld);
       if (e.tokens > 0 && e.table == e.y) c.refuse("grad must not be dy");
     }

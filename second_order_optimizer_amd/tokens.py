@@ -186,7 +186,7 @@ class Embedding(_Operator):
 
     dtype: "bf16" or "f32", of the rows; table_dtype: of the table and its
     gradient (default: the rows').  Where the table requires grad, the result
-    is part of autograd's graph.
+    is part of autograd's graph; tensors with a forward-mode tangent are refused.
     """
 
     def __init__(self, rows: int, vocab: int, width: int, dtype: str = "bf16", table_dtype: Optional[str] = None,
