@@ -158,7 +158,8 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const DropoutPlan* plan = plan_of<DropoutPlan>(a, n, 7);
     Call c(plan->base);
     kfac_dropout_t d = plan->d;
-    const at::Tensor& x = c.tensor(a[1], "x");
+    const at::Tensor& x = c.differentiable(a[1], "x");
+    if (a[4] != Py_None) c.differentiable(a[4], "residual");
     if (c10::GradMode::is_enabled() &&
         (x.requires_grad() || (a[4] != Py_None && c.tensor(a[4], "residual").requires_grad()))) {
       if (a[5] != Py_None) c.refuse("out cannot be given where x or residual requires grad");
@@ -171,7 +172,7 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[4] != Py_None) d.residual = c.matrix(c.tensor(a[4], "residual"), "residual", d.rows, d.cols, &d.residual_ld);
     at::Tensor y;
     if (a[5] != Py_None) {
-      y = c.tensor(a[5], "out");
+      y = c.differentiable(a[5], "out");
       c.matrix(y, "out", d.rows, d.cols, &d.y_ld);
     }
     if (a[6] != Py_None) d.offset_dev = static_cast<const int64_t*>(c.vector(a[6], "offset_tensor", 1, at::kLong));

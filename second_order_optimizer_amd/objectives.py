@@ -345,7 +345,7 @@ class _DropoutNode(torch.autograd.Function):
 class Dropout(_Operator):
     """Dropout whose mask is a function of (seed, offset, position): kept with probability 1 - p, scaled
     by 1 / (1 - p) (p to 16 bits), nothing stored between forward and backward.  Where x or residual
-    requires grad, the result is part of autograd's graph."""
+    requires grad, the result is part of autograd's graph; tensors with a forward-mode tangent are refused."""
 
     def __init__(self, rows: int, cols: int, dtype: str = "bf16", p: float = 0.1, device="cuda"):
         super().__init__(_DropoutPlan(), dtype, device)

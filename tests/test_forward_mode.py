@@ -7,6 +7,7 @@ import torch
 from torch.autograd import forward_ad as F
 
 import second_order_optimizer_amd as K
+from second_order_optimizer_amd import objectives as O
 from second_order_optimizer_amd import tokens as T
 
 
@@ -44,3 +45,18 @@ def test_embedding():
             refused("GPU only", op.run, dual(8, 16), ids)
     with pytest.raises(Exception):
         torch.func.jvp(lambda t: op.run(t, ids), (table,), (table,))
+
+
+def test_dropout():
+    op = O.Dropout(4, 16, dtype="f32", p=0.5, device="cpu")
+    x = torch.zeros(4, 16)
+    refused("GPU only", op.run, x, 1, residual=x)
+    with F.dual_level():
+        refused("tangent", op.run, dual(4, 16), 1)
+        refused("tangent", op.run, F.make_dual(torch.zeros(4, 16, requires_grad=True), torch.ones(4, 16)), 1)
+        refused("tangent", op.run, x, 1, residual=dual(4, 16))
+        refused("tangent", op.run, x, 1, out=dual(4, 16))
+        refused("tangent", op.backward, dual(4, 16), 1)
+        refused("GPU only", op.run, x, 1, residual=x)
+    with pytest.raises(Exception):
+        torch.func.jvp(lambda t: op.run(t, 1), (x,), (x,))
