@@ -107,7 +107,9 @@ PyObject* embedding_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (e.tokens > 0 && e.table == e.y) c.refuse("grad must not be dy");
     }
     const bool given = grad.defined();
-    e.accumulate = a[4] == Py_True;
+    const int accumulate = PyObject_IsTrue(a[4]);
+    if (accumulate < 0) return nullptr;
+    e.accumulate = accumulate;
     if (e.accumulate && !given) c.refuse("accumulate needs grad");
     void* stream = c.enter();
     at::Tensor counts = c.make(e.vocab, at::kInt);
