@@ -93,7 +93,7 @@ kfac_status_t kfac_orthogonalize(const kfac_orthogonal_matrix_t* m, const kfac_o
  * their element).  A bias has no matrix to orthogonalise and takes the step
  * that it takes in kfac.h with D its gradient:
  *     V <- mu V + (grad_b + wd b);   b <- b - lr V
- * Layers must not share tensors, and no gradient may be a tensor that is written.
+ * What is written must not share memory, with itself or with a gradient: KFAC_ERR_ARG.
  */
 kfac_status_t kfac_step_orthogonal(const kfac_layer_t* layers, int32_t n_layers, const kfac_hparams_t* hp,
                                    const kfac_orthogonal_t* how, void* workspace, size_t ws_bytes, void* stream);

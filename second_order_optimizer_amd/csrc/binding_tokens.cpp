@@ -3,6 +3,7 @@
 // address of an operator's plan, mirrored by tokens.py and orthogonal.py, and
 // tensors or None, runs on the device's current stream and returns the outputs.
 #include "binding.h"
+#include "overlap.h"
 
 #include "../../include/kfac_orthogonal.h"
 #include "../../include/kfac_tokens.h"
@@ -215,15 +216,15 @@ PyObject* orthogonal_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
           int64_t ld;
           L.grad_w = static_cast<const float*>(c.matrix(g, name, L.d_out, L.d_in, &ld));
           if (ld != L.d_in) c.refuse("grads must be contiguous");
-          if (L.grad_w == L.w || L.grad_w == L.mom_w) c.refuse("grads must not be weights or momenta");
         } else if (L.has_bias) {
           L.grad_b = static_cast<const float*>(c.vector(o, name, L.d_out, at::kFloat));
-          if (L.grad_b == L.b || L.grad_b == L.mom_b) c.refuse("bias_grads must not be biases or their momenta");
         } else if (o != Py_None) {
           c.refuse("bias_grads must be None for a layer without bias");
         }
       }
     }
+    if (kfac::step_shares_memory(plan->layers, plan->n))
+      c.refuse("weights, momenta and biases must not share memory, and no gradient may share theirs");
     void* stream = c.enter();
     done(entries.step(plan->layers, static_cast<int32_t>(plan->n), &hp, &plan->how, plan->base.ws, plan->base.ws_bytes, stream),
          "kfac_step_orthogonal");

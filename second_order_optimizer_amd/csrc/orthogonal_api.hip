@@ -1,6 +1,7 @@
 // The extern "C" entry points of include/kfac_orthogonal.h: host-side
 // validation and dispatch.
 #include "orthogonal.h"
+#include "overlap.h"
 #include "validate.h"
 
 #include <algorithm>
@@ -169,6 +170,7 @@ kfac_status_t kfac_step_orthogonal(const kfac_layer_t* layers, int32_t n_layers,
   if (p.s != KFAC_OK) return p.s;
   s = kfac::check_workspace(workspace, ws_bytes, kfac::orth_workspace_bytes(tasks, *how));
   if (s != KFAC_OK) return s;
+  if (kfac::step_shares_memory(layers, n_layers)) return KFAC_ERR_ARG;
   return kfac::launch_orthogonal(tasks, *how, kfac::OrthStep{hp->lr, hp->momentum, hp->weight_decay},
                                  static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
 }

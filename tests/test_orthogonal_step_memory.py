@@ -77,3 +77,32 @@ def test_step_of_weights_that_moved(gpu_lib):
         for t, u in zip(now, v):
             assert t is None or torch.equal(t, u)
     assert all(torch.equal(t, u) for t, u in zip(old, was))
+
+
+def test_gradients_that_are_written(lib):
+    """A gradient that is another layer's weight, momentum or bias, whole or in part, and tensors that came to share
+    memory later."""
+    w, m, b, bm, g, bg = layers()
+    s = M.OrthogonalStep(w, m, b, bm)
+    room = torch.randn(100)
+    w[2].data = room[50:59].view(3, 3)
+    refused(U, s.run, g, bg)                                                 # valid, but not on a GPU
+    for i, bad in ((2, w[2]), (2, m[2]), (2, room[46:55].view(3, 3)), (2, room[58:67].view(3, 3)), (0, room[30:62].view(4, 8)),
+                   (0, w[0]), (0, m[0])):
+        refused(A, s.run, [bad if j == i else t for j, t in enumerate(g)], bg)
+    for i, bad in ((0, b[0]), (0, bm[0]), (2, b[0][:3]), (2, bm[0][1:]), (0, room[55:59])):
+        refused(A, s.run, g, [bad if j == i else t for j, t in enumerate(bg)])
+    refused(A, s.run, [g[0], g[1], w[0].view(-1)[:9].view(3, 3)], bg)        # of another layer
+    refused(U, s.run, [g[0], g[1], room[41:50].view(3, 3)], bg)              # beside it
+    refused(U, s.run, [g[0], g[1], g[0].view(-1)[:9].view(3, 3)], bg)        # gradients are only read
+    w[2].data = m[0].view(-1)[:9].view(3, 3)
+    refused(A, s.run, g, bg)
+
+
+@pytest.mark.parametrize("over", [dict(grad_w=0x30000), dict(grad_w=0x20000 + 4 * 6999), dict(grad_b=0x50004), dict(mom_b=0x50000 + 4 * 99),
+                                  dict(w=0x70000, mom_w=0x70000 + 4 * 14), dict(w=0x10000 + 4 * 6999), dict(b=0x40000)])
+def test_shared_memory_at_the_c_entry(lib, over):
+    """The second of two layers on memory of the first, or on its own (addresses that are never read)."""
+    from tests.test_tokens_abi import layer, step
+    apart = dict(d_in=3, d_out=5, grad_w=0x100000, w=0x110000, mom_w=0x120000, grad_b=0x130000, b=0x140000, mom_b=0x150000)
+    assert step(lib, [layer(), layer(**{**apart, **over})]) == A
