@@ -88,7 +88,8 @@ typedef struct kfac_sample {
  * not occur have zeros.  With accumulate set, the sum is added to what grad
  * holds, and rows of tokens that do not occur are not touched.  counts /
  * tokens is the diagonal of the factor A of a layer whose inputs are one-hot
- * rows.  What is written must not overlap what is read (but for accumulate).
+ * rows.  What is written must not share memory with what is read, but for
+ * accumulate (between the rows of it is beside it): KFAC_ERR_ARG.
  */
 typedef struct kfac_embedding {
   void* table;             /* [vocab, width] of table_dtype, row stride table_ld: read by lookup, and

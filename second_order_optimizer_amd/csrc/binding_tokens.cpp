@@ -64,6 +64,13 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The memory of a tensor that has passed its checks: adjacent columns.
+kfac::Lines lines_of(const at::Tensor& t) {
+  const int64_t el = t.element_size(), d = t.dim();
+  return kfac::lines_of(t.data_ptr(), t.numel() ? t.size(d - 1) * el : 0, d > 1 ? t.size(d - 2) : 1, d > 1 ? t.stride(d - 2) * el : 0,
+                        d > 2 ? t.size(0) : 1, d > 2 ? t.stride(0) * el : 0);
+}
+
 // (plan, table, ids, out) -> y, or None (and nothing done) where the call belongs into autograd's graph
 PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -81,7 +88,9 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[3] != Py_None) {
       y = c.differentiable(a[3], "out");
       c.matrix(y, "out", e.tokens, e.width, &e.y_ld);
-      if (e.tokens > 0 && y.data_ptr() == e.table) c.refuse("out must not be table");
+      const kfac::Lines to = lines_of(y);
+      if (kfac::overlap(to, lines_of(table)) || kfac::overlap(to, lines_of(c.tensor(a[2], "ids"))))
+        c.refuse("out must not share memory with table or ids");
     }
     const bool given = y.defined();
     void* stream = c.enter();
@@ -105,7 +114,9 @@ PyObject* embedding_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[3] != Py_None) {
       grad = c.differentiable(a[3], "grad");
       e.table = c.matrix_of(grad, "grad", e.table_dtype, e.vocab, e.width, &e.table_ld);
-      if (e.tokens > 0 && e.table == e.y) c.refuse("grad must not be dy");
+      const kfac::Lines to = lines_of(grad);
+      if (kfac::overlap(to, lines_of(c.tensor(a[1], "dy"))) || kfac::overlap(to, lines_of(c.tensor(a[2], "ids"))))
+        c.refuse("grad must not share memory with dy or ids");
     }
     const bool given = grad.defined();
     const int accumulate = PyObject_IsTrue(a[4]);

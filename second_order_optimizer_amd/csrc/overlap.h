@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <numeric>
 #include <vector>
 
 #include "../../include/kfac.h"
@@ -47,6 +48,33 @@ inline bool step_shares_memory(const kfac_layer_t* layers, int64_t n) {
     spans.push_back(span_of(L.grad_b, bias, false));
   }
   return share_memory(spans);
+}
+
+// Strided memory: `mats` matrices of `rows` rows of `run` bytes, rows `ld` and matrices
+// `stride` bytes apart.
+struct Lines {
+  uintptr_t begin;
+  int64_t run, rows, ld, mats = 1, stride = 0;
+};
+inline Lines lines_of(const void* p, int64_t run, int64_t rows = 1, int64_t ld = 0, int64_t mats = 1, int64_t stride = 0) {
+  return {reinterpret_cast<uintptr_t>(p), run, rows, ld, mats, stride};
+}
+
+// Whether the two may share memory.  No where their extents do not meet, and none where
+// all distances are multiples of one number (as between column slices of a matrix) and
+// the runs lie apart within it; what neither shows apart counts as shared.
+inline bool overlap(const Lines& a, const Lines& b) {
+  auto extent = [](const Lines& l) { return l.run + (l.rows - 1) * l.ld + (l.mats - 1) * l.stride; };
+  if (a.run < 1 || a.rows < 1 || a.mats < 1 || b.run < 1 || b.rows < 1 || b.mats < 1) return false;
+  if (a.begin + static_cast<uintptr_t>(extent(a)) <= b.begin || b.begin + static_cast<uintptr_t>(extent(b)) <= a.begin) return false;
+  int64_t g = 0;
+  for (const Lines* l : {&a, &b}) {
+    if (l->rows > 1) g = std::gcd(g, l->ld);
+    if (l->mats > 1) g = std::gcd(g, l->stride);
+  }
+  if (g == 0) return true;
+  const int64_t apart = static_cast<int64_t>(b.begin - a.begin) % g, d = apart < 0 ? apart + g : apart;
+  return d < a.run || d + b.run > g;
 }
 
 }  // namespace kfac

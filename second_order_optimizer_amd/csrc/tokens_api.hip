@@ -1,5 +1,6 @@
 // The extern "C" entry points of include/kfac_tokens.h: host-side validation
 // and dispatch.
+#include "overlap.h"
 #include "tokens.h"
 #include "validate.h"
 
@@ -18,6 +19,16 @@ kfac_status_t check_embedding(const kfac_embedding_t* e) {
   if (!extent_ok(e->vocab, e->table_ld) || !extent_ok(e->tokens, e->y_ld)) return KFAC_ERR_UNSUPPORTED;
   return KFAC_OK;
 }
+
+Lines table_lines(const kfac_embedding_t* e) {
+  const int64_t el = elem_size(e->table_dtype);
+  return lines_of(e->table, e->width * el, e->vocab, e->table_ld * el);
+}
+Lines row_lines(const kfac_embedding_t* e) {
+  const int64_t el = elem_size(e->dtype);
+  return lines_of(e->y, e->width * el, e->tokens, e->y_ld * el);
+}
+Lines id_lines(const kfac_embedding_t* e) { return lines_of(e->ids, e->tokens * static_cast<int64_t>(index_size(e->id_type))); }
 
 }  // namespace
 }  // namespace kfac
@@ -78,6 +89,7 @@ kfac_status_t kfac_embedding_lookup(const kfac_embedding_t* e, void* workspace, 
   }
   s = kfac::check_workspace(workspace, ws_bytes, kfac::kRegions);
   if (s != KFAC_OK) return s;
+  if (kfac::overlap(kfac::row_lines(e), kfac::table_lines(e)) || kfac::overlap(kfac::row_lines(e), kfac::id_lines(e))) return KFAC_ERR_ARG;
   return kfac::launch_embedding_lookup(*e, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
 }
 
@@ -94,6 +106,10 @@ kfac_status_t kfac_embedding_grad(const kfac_embedding_t* e, void* workspace, si
   if (p.s != KFAC_OK) return p.s;
   s = kfac::check_workspace(workspace, ws_bytes, kfac::embedding_workspace_bytes(e->tokens, e->vocab, e->width));
   if (s != KFAC_OK) return s;
+  const kfac::Lines table = kfac::table_lines(e), counts = kfac::lines_of(e->counts, e->counts ? 4 * static_cast<int64_t>(e->vocab) : 0);
+  for (const kfac::Lines& read : {kfac::row_lines(e), kfac::id_lines(e)})
+    if (kfac::overlap(table, read) || kfac::overlap(counts, read)) return KFAC_ERR_ARG;
+  if (kfac::overlap(table, counts)) return KFAC_ERR_ARG;
   return kfac::launch_embedding_grad(*e, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
 }
 

@@ -48,3 +48,90 @@ def test_accumulate_by_a_number(gpu_lib):
         grad = torch.full((8, 16), 5.0, device="cuda")
         op.backward(dy, ids, grad=grad, accumulate=yes)
         assert grad[:, 0].tolist() == [5, 7, 5, 6, 5, 5, 5, 5]
+
+
+def test_outputs_on_memory_that_is_read():
+    """What is written may lie beside what is read, between its rows as well, and nowhere on it."""
+    op = T.Embedding(4, 8, 16, dtype="f32", device="cpu")
+    room, ids = torch.zeros(4000), torch.zeros(4, dtype=torch.int64)
+    table, wide, dy = room[:128].view(8, 16), room[1000:1000 + 8 * 40].view(8, 40), torch.zeros(4, 16)
+    at = lambda n: room[n:n + 64].view(4, 16)  # noqa: E731
+    for out in (at(0), at(64), at(16), at(127), at(3), wide[:4, :16], wide[4:, 8:24], wide[:4, 0:16]):
+        base = table if out.data_ptr() < wide.data_ptr() else wide[:, 0:16]
+        refused(A, op.run, base, ids, out=out)
+    for out in (at(128), at(500), wide[:4, 16:32], wide[4:, 24:40]):
+        refused(U, op.run, wide[:, 0:16] if out.data_ptr() >= wide.data_ptr() else table, ids, out=out)
+    refused(U, op.run, wide[:, 24:40], ids, out=wide[:4, 0:16])
+    refused(A, op.run, table, room[2000:2008].view(torch.int64), out=at(2005))
+    for bad, ok in ((at(0), at(128)), (at(64), at(900))):
+        refused(A, op.backward, bad, ids, grad=table)
+        refused(U, op.backward, ok, ids, grad=table)
+    refused(A, op.backward, wide[:4, 10:26], ids, grad=wide[:, 0:16], accumulate=True)
+    refused(U, op.backward, wide[:4, 16:32], ids, grad=wide[:, 0:16], accumulate=True)
+    refused(A, op.backward, dy, room[2000:2008].view(torch.int64), grad=room[1900:2028].view(8, 16))
+    none = T.Embedding(0, 8, 16, dtype="f32", device="cpu")
+    refused(U, none.run, table, ids[:0], out=table[:0])
+
+
+@pytest.mark.parametrize("fn,over", [("lookup", dict(y=0x10000 + 508)), ("lookup", dict(y=0x30000 + 30)), ("lookup", dict(y=0x10020, table_ld=24, y_ld=48)),
+                                     ("grad", dict(y=0x10000 + 500)), ("grad", dict(counts=0x10000)), ("grad", dict(counts=0x20000)),
+                                     ("grad", dict(counts=0x30000)), ("grad", dict(ids=0x10000))])
+def test_shared_memory_at_the_c_entries(lib, fn, over):
+    from tests.test_tokens_abi import call, embedding
+    assert call(getattr(lib, "kfac_embedding_" + fn), embedding(**over)) == A
+
+
+def test_overlap_against_every_byte(tmp_path):
+    """csrc/overlap.h on small matrices: never apart where a byte is shared; never shared for column slices of one
+    matrix, or for what lies side by side, where none is."""
+    import itertools
+    import shutil
+    import subprocess
+    if not shutil.which("g++"):
+        pytest.skip("g++ not installed")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src, exe = tmp_path / "overlap.cpp", tmp_path / "overlap"
+    src.write_text('#include <cstdio>\n#include <set>\n#include "%s"\n' % os.path.join(root, "second_order_optimizer_amd", "csrc", "overlap.h") + """
+int main() {
+  long long at, run, rows, ld, mats, stride;
+  kfac::Lines l[2];
+  for (;;) {
+    std::set<long long> bytes;
+    bool shared = false;
+    for (int i = 0; i < 2; ++i) {
+      if (std::scanf("%lld %lld %lld %lld %lld %lld", &at, &run, &rows, &ld, &mats, &stride) != 6) return 0;
+      l[i] = kfac::lines_of(reinterpret_cast<void*>(at), run, rows, ld, mats, stride);
+      for (long long m = 0; m < mats; ++m)
+        for (long long r = 0; r < rows; ++r)
+          for (long long c = 0; c < run; ++c) {
+            const long long b = at + m * stride + r * ld + c;
+            if (i) shared |= bytes.count(b) != 0;
+            else bytes.insert(b);
+          }
+    }
+    std::printf("%d %d\\n", shared, kfac::overlap(l[0], l[1]));
+  }
+}
+""")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", str(src), "-o", str(exe)], check=True)
+    rng = np.random.default_rng(0)
+    cases = []
+    for _ in range(4000):
+        pair = []
+        for _ in range(2):
+            run, rows, mats = (int(rng.integers(0, n)) for n in (7, 5, 3))
+            ld = run + int(rng.integers(0, 9))
+            pair.append((1000 + int(rng.integers(0, 60)), run, rows, ld, mats, rows * ld + int(rng.integers(0, 9))))
+        cases.append((pair, False))
+    for a, b, at in itertools.product(range(1, 5), range(1, 5), range(0, 80, 3)):      # of one matrix of 11 columns
+        cases.append(([(1000, a, 4, 11, 1, 0), (1000 + at, b, 3, 11, 1, 0)], True))
+    text = "\n".join(" ".join(map(str, v)) for pair, _ in cases for v in pair)
+    out = subprocess.run([str(exe)], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
+    for (pair, exact), line in zip(cases, out):
+        shared, said = (v == "1" for v in line.split())
+        assert said or not shared, pair
+        (pa, ra, na, la, ma, _), (pb, rb, nb, lb, mb, _) = pair
+        inside = (pb - pa) % 11 + rb <= 11                              # the second matrix's rows are whole columns of the first's
+        if exact and inside and pb - pa < 33:
+            assert said == shared, pair
+    assert any(line == "0 0" for line in out) and any(line == "1 1" for line in out)
