@@ -61,7 +61,8 @@ typedef struct kfac_orthogonal {
 
 /* A batch of matrices, row-major, rows `ld` elements and matrices `stride`
  * elements apart.  y may be x itself with the same strides, and must not
- * overlap it otherwise.  Pointers need the alignment of their element. */
+ * share memory with it otherwise: KFAC_ERR_ARG.  Pointers need the alignment of
+ * their element. */
 typedef struct kfac_orthogonal_matrix {
   const void* x;        /* [batch, rows, cols] of dtype */
   void* y;              /* likewise, written */

@@ -142,6 +142,10 @@ kfac_status_t kfac_orthogonalize(const kfac_orthogonal_matrix_t* m, const kfac_o
   const std::vector<kfac::OrthTask> tasks{kfac::task_of(*m)};
   s = kfac::check_workspace(workspace, ws_bytes, kfac::orth_workspace_bytes(tasks, *how));
   if (s != KFAC_OK || m->batch == 0) return s;
+  const int64_t el = static_cast<int64_t>(kfac::elem_size(m->dtype));
+  const kfac::Lines x = kfac::lines_of(m->x, m->cols * el, m->rows, m->ld * el, m->batch, m->stride * el);
+  const kfac::Lines y = kfac::lines_of(m->y, m->cols * el, m->rows, m->y_ld * el, m->batch, m->y_stride * el);
+  if (m->x != m->y && kfac::overlap(x, y)) return KFAC_ERR_ARG;
   return kfac::launch_orthogonal(tasks, *how, kfac::OrthStep{}, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
 }
 

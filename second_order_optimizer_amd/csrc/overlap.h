@@ -60,21 +60,26 @@ inline Lines lines_of(const void* p, int64_t run, int64_t rows = 1, int64_t ld =
   return {reinterpret_cast<uintptr_t>(p), run, rows, ld, mats, stride};
 }
 
-// Whether the two may share memory.  No where their extents do not meet, and none where
-// all distances are multiples of one number (as between column slices of a matrix) and
-// the runs lie apart within it; what neither shows apart counts as shared.
+// Whether the two may share memory.  Not where their extents do not meet, nor where all
+// distances between their rows (or matrices) are multiples of one number, as between
+// column slices of a matrix (row slices of a batch), and the rows (matrices) lie apart
+// within it; what none of this shows apart counts as shared.
 inline bool overlap(const Lines& a, const Lines& b) {
-  auto extent = [](const Lines& l) { return l.run + (l.rows - 1) * l.ld + (l.mats - 1) * l.stride; };
   if (a.run < 1 || a.rows < 1 || a.mats < 1 || b.run < 1 || b.rows < 1 || b.mats < 1) return false;
+  auto matrix = [](const Lines& l) { return l.run + (l.rows - 1) * l.ld; };
+  auto extent = [&](const Lines& l) { return matrix(l) + (l.mats - 1) * l.stride; };
   if (a.begin + static_cast<uintptr_t>(extent(a)) <= b.begin || b.begin + static_cast<uintptr_t>(extent(b)) <= a.begin) return false;
-  int64_t g = 0;
+  auto apart = [&](int64_t a_run, int64_t b_run, int64_t step) {      // runs `step`, or a multiple of it, apart
+    if (step == 0) return false;
+    const int64_t d = (static_cast<int64_t>(b.begin - a.begin) % step + step) % step;
+    return d >= a_run && d + b_run <= step;
+  };
+  int64_t rows = 0, mats = 0;
   for (const Lines* l : {&a, &b}) {
-    if (l->rows > 1) g = std::gcd(g, l->ld);
-    if (l->mats > 1) g = std::gcd(g, l->stride);
+    if (l->rows > 1) rows = std::gcd(rows, l->ld);
+    if (l->mats > 1) mats = std::gcd(mats, l->stride);
   }
-  if (g == 0) return true;
-  const int64_t apart = static_cast<int64_t>(b.begin - a.begin) % g, d = apart < 0 ? apart + g : apart;
-  return d < a.run || d + b.run > g;
+  return !apart(a.run, b.run, std::gcd(rows, mats)) && !apart(matrix(a), matrix(b), mats);
 }
 
 }  // namespace kfac

@@ -81,6 +81,23 @@ def test_shared_memory_at_the_c_entries(lib, fn, over):
     assert call(getattr(lib, "kfac_embedding_" + fn), embedding(**over)) == A
 
 
+def test_update_beside_and_on_its_input(lib):
+    """out: x itself with its strides, or memory that it has no part of."""
+    op = M.Orthogonal(4, 8, batch=2, dtype="f32", device="cpu")
+    room = torch.zeros(3, 10, 20)
+    x = room[:2, 2:6, 4:12]
+    for out in (x, room[:2, 2:6, 12:20], room[:2, 6:10, 4:12], torch.zeros(2, 4, 8)):
+        refused(U, op.run, x, out=out)
+    for out in (room[:2, 3:7, 4:12], room[:2, 2:6, 5:13], room[1:, 2:6, 4:12], room[:2, 2:6, 0:8], room.view(-1)[44:108].view(2, 4, 8)):
+        refused(A, op.run, x, out=out)
+    one = M.Orthogonal(4, 8, dtype="f32", device="cpu")
+    refused(A, one.run, room[0, :4, :8], out=room[0, 1:5, :8])
+    refused(U, one.run, room[0, :4, :8], out=room[0, 4:8, :8])
+    from tests.test_tokens_abi import how, matrix, orthogonalize
+    for over in (dict(y=0x10004), dict(y=0x10000 + 4 * (70 * 200 - 1)), dict(y=0x10000 - 4 * (70 * 200 - 1)), dict(y=0x10000 + 4 * 7000)):
+        assert orthogonalize(lib, matrix(**over), how()) == A, over
+
+
 def test_overlap_against_every_byte(tmp_path):
     """csrc/overlap.h on small matrices: never apart where a byte is shared; never shared for column slices of one
     matrix, or for what lies side by side, where none is."""
