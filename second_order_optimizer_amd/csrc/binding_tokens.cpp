@@ -169,7 +169,8 @@ PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[2] != Py_None) {
       y = c.tensor(a[2], "out");
       m.y = stack_of(c, y, "out", m, &m.y_ld, &m.y_stride);
-      if (m.y != m.x && kfac::overlap(lines_of(y), lines_of(x))) c.refuse("out must be x itself, or share no memory with it");
+      const bool same = m.y == m.x && m.y_ld == m.ld && m.y_stride == m.stride;
+      if (!same && kfac::overlap(lines_of(y), lines_of(x))) c.refuse("out must be x itself, or share no memory with it");
     }
     const bool given = y.defined();
     void* stream = c.enter();
