@@ -169,7 +169,7 @@ PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[2] != Py_None) {
       y = c.tensor(a[2], "out");
       m.y = stack_of(c, y, "out", m, &m.y_ld, &m.y_stride);
-      const bool same = m.y == m.x && m.y_ld == m.ld && m.y_stride == m.stride;
+      const bool same = m.y == m.x && m.y_ld == m.ld && (m.batch < 2 || m.y_stride == m.stride);
       if (!same && kfac::overlap(lines_of(y), lines_of(x))) c.refuse("out must be x itself, or share no memory with it");
     }
     const bool given = y.defined();

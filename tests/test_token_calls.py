@@ -93,6 +93,7 @@ def test_update_beside_and_on_its_input(lib):
     one = M.Orthogonal(4, 8, dtype="f32", device="cpu")
     refused(A, one.run, room[0, :4, :8], out=room[0, 1:5, :8])
     refused(U, one.run, room[0, :4, :8], out=room[0, 4:8, :8])
+    refused(U, one.run, room[0, :4, :8], out=room[:1, :4, :8])              # itself, as a batch of one
     from tests.test_tokens_abi import how, matrix, orthogonalize
     for over in (dict(y=0x10004), dict(y=0x10000 + 4 * (70 * 200 - 1)), dict(y=0x10000 - 4 * (70 * 200 - 1)), dict(y=0x10000 + 4 * 7000)):
         assert orthogonalize(lib, matrix(**over), how()) == A, over
