@@ -36,11 +36,17 @@ extern "C" {
 #endif
 
 /* kfac_orthogonal_t.products: what the iteration's matrices are held in
- * between its products, whose sums are float32 either way.
- *   HALF  11 bits (IEEE half, scaled): O within 1e-3 of 64 bits (2-norm,
- *         relative; bfloat16's own rounding is 1.7e-3)
- *   FULL  22 bits (two halves, three products each): within 5e-6, as float32
- *         products are (2e-5 where a few directions make up nearly all of x)
+ * between its products, whose sums are float32 either way.  O is then off that
+ * of 64 bits by (2-norm, relative):
+ *   HALF  11 bits (IEEE half, scaled).  5e-4 to 1.2e-3 for noise with or without
+ *         strong directions over it (bfloat16's own rounding is 1.7e-3); up to
+ *         4e-3 for sparse matrices, 1e-2 for equal singular values (an
+ *         identity), whose roundings are all the same, and 1.2e-2 where a few
+ *         directions make up all of x and its shorter side is below 300: of the
+ *         others there are then hardly any but roundings, and they are what grows
+ *   FULL  22 bits (two halves, three products each).  What float32 products are
+ *         off: 1e-6 to 5e-6, and where a few directions make up nearly all of x
+ *         up to 3e-4 (shorter sides up to 1024)
  * Matrices with a side of at most 64 take neither: they are iterated in 64 bits. */
 enum { KFAC_PRODUCTS_HALF = 0, KFAC_PRODUCTS_FULL = 1 };
 /* kfac_orthogonal_t.scale: the factor s of a layer's step, W [d_out, d_in]

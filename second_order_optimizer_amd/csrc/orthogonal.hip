@@ -19,8 +19,10 @@
 // low halves, for the term a X: where a few strong directions make up most of X,
 // its rounding to 11 bits is large against all the others, which that term
 // carries; as operands of the products, where B hardly has them yet, 11 bits do.
-// (Both together: 1.5e-3 -> 5e-4 of the result.)  bfloat16 outputs take HALF,
-// float32 ones FULL.  Each matrix carries a power of two that keeps |value| <= 2^15:
+// (Both together: 1.5e-3 -> 5e-4 of the result.  Where x has a few directions and
+// nothing else the diagonal apart costs, as the operand's roundings then reach the
+// others through it: 6e-4 -> 1.6e-3 for eight of 128 x 128.)  bfloat16 outputs take
+// HALF, float32 ones FULL.  Each matrix carries a power of two that keeps |value| <= 2^15:
 // the norm bounds every element, and the polynomial's maximum bounds the norm after
 // each step.
 //
@@ -31,7 +33,7 @@
 // one product with X, one X X^T and five d x d ones (symmetric all, as the factors
 // are polynomials of A) in place of two, two and two; an odd step stays by itself.
 // In 22 bits that is as exact (2e-6 of the result where a step at a time is 1e-6,
-// both 2e-5 where eight directions make up nearly all of X); in 11 bits it would
+// both 2e-5 to 5e-5 where eight directions make up nearly all of X); in 11 bits it would
 // double the error, so HALF takes a step at a time.  Eight layers of 1024 x 4096:
 // 2.51 -> 2.01 ms.
 //

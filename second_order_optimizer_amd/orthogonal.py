@@ -104,7 +104,9 @@ class Orthogonal(_Iteration):
     rows, cols, batch: the shape of x.  dtype: "bf16" or "f32", of x and the
     result.  coefs: (a, b, c) of every step, or one such triple a step.
     products: "half" holds the iteration's matrices in 11 bits (the default
-    for bf16), "full" in 22 (for f32).
+    for bf16; off by 5e-4 to 1.2e-3, and by up to 1.2e-2 for matrices without
+    rank or with equal singular values), "full" in 22 (for f32; as exact as
+    float32 products make it).
     """
 
     def __init__(self, rows: int, cols: int, batch: int = 1, dtype: str = "bf16", steps: int = 5, coefs=COEFS,
@@ -140,8 +142,8 @@ class OrthogonalStep(_Iteration):
     one.  nesterov: whether the update looks ahead by the momentum.  scale:
     the factor of a layer's step, "aspect" sqrt(max(1, d_out / d_in)), "rms"
     0.2 sqrt(max(d_out, d_in)) or "none" 1.  products: "full" (the update as
-    exact as float32 products make it) or "half" (within 1e-3, a third of the
-    operations).
+    exact as float32 products make it) or "half" (11 bits between the products,
+    a third of the operations; Orthogonal says how far off).
     """
 
     def __init__(self, weights: Sequence, momenta: Sequence, biases: Optional[Sequence] = None,
