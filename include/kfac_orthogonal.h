@@ -45,8 +45,8 @@ extern "C" {
  *         directions make up all of x and its shorter side is below 300: of the
  *         others there are then hardly any but roundings, and they are what grows
  *   FULL  22 bits (two halves, three products each).  What float32 products are
- *         off: 1e-6 to 5e-6, and where a few directions make up nearly all of x
- *         up to 3e-4 (shorter sides up to 1024)
+ *         off: 1e-6 to 5e-6 (sides of more than 4096: to 1e-5), and where a few
+ *         directions make up nearly all of x up to 3e-4 (shorter sides up to 1024)
  * Matrices with a side of at most 64 take neither: they are iterated in 64 bits. */
 enum { KFAC_PRODUCTS_HALF = 0, KFAC_PRODUCTS_FULL = 1 };
 /* kfac_orthogonal_t.scale: the factor s of a layer's step, W [d_out, d_in]
