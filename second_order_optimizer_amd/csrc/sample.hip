@@ -168,10 +168,9 @@ struct Row {
 };
 
 constexpr int kOwn = 32;                  // bins of a thread's own histogram
-template <int NT>
-constexpr int kList = 4 * NT;             // listed columns, in the histograms' LDS
 
-// A listed column and its mass: sixteen bytes, one read.
+// A listed column and its mass: sixteen bytes, one read.  A list has a column a thread
+// at most, and lies in the histograms' LDS.
 struct alignas(16) Listed {
   uint64_t place, mass;
 };
@@ -509,7 +508,7 @@ __device__ __forceinline__ bool draw_of_few(Shared<NT>& s, Listed* list, Row<T, 
 template <typename T, int NT, bool HELD>
 __device__ __forceinline__ bool border_of_mass(Shared<NT>& s, float* own, uint64_t* block_mass, Row<T, NT, HELD>& row, const Scale& sc,
                                                double p, int vocab, Border* out) {
-  constexpr int VE = Elem<T>::VE, LIST = kList<NT>;
+  constexpr int VE = Elem<T>::VE;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const float cf = static_cast<float>(sc.c);
   // columns of less than (1 - p) / vocab of the maximum's weight together weigh less
@@ -578,7 +577,7 @@ __device__ __forceinline__ bool border_of_mass(Shared<NT>& s, float* own, uint64
         ++kept;
       } else if (at < above + 1.f && in < part + 1.f) {
         const uint32_t to = atomicAdd(&s.listed, 1u);
-        if (to < LIST) list[to].place = place_of(x, row.column(j, i));
+        if (to < NT) list[to].place = place_of(x, row.column(j, i));
       }
     }
     above_own += mass;
@@ -819,7 +818,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   extern __shared__ uint64_t block_mass[];         // kept mass of each block of NT vectors
   __shared__ Listed lists[CUT ? kOwn * NT / 4 : 1];        // or the threads' histograms
   float* histograms = reinterpret_cast<float*>(lists);
-  static_assert(kOwn * NT * sizeof(float) >= kList<NT> * sizeof(Listed));
+  static_assert(kOwn * NT * sizeof(float) >= NT * sizeof(Listed));
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   Row<T, NT, HELD> row;
