@@ -153,3 +153,35 @@ int main() {
         if exact and inside and pb - pa < 33:
             assert said == shared, pair
     assert any(line == "0 0" for line in out) and any(line == "1 1" for line in out)
+
+
+@pytest.mark.gpu
+def test_capture_beside_a_graph_of_another_stream(gpu_lib):
+    """What the refusal of a captured lookup advises: an eager graph of the same table, made on a stream of its own, may
+    live while a lookup and its backward pass are captured; replays with eager work between them."""
+    op, other = (T.Embedding(5, 9, 16, "f32") for _ in range(2))
+    table, ids = torch.randn(9, 16, device="cuda", requires_grad=True), torch.tensor([0, 3, 3, -1, 8], device="cuda")
+    counts = torch.tensor([1.0, 0, 0, 2, 0, 0, 0, 0, 1], device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        eager = other.run(table, ids)
+    torch.cuda.synchronize()
+    table.grad = torch.zeros_like(table)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        table.grad.zero_()
+        y = op.run(table, ids)
+        y.backward(torch.full_like(y, 2.0))
+    for i in range(3):
+        with torch.no_grad():
+            table.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y[[0, 1, 2, 4]], table.detach()[ids[[0, 1, 2, 4]]]) and (y[3] == 0).all()
+        assert torch.equal(table.grad, 2 * counts[:, None].expand(9, 16)), i
+    with torch.cuda.stream(side):
+        table.grad.zero_()
+        eager.backward(torch.ones_like(eager))
+    torch.cuda.synchronize()
+    assert torch.equal(table.grad, counts[:, None].expand(9, 16))
