@@ -8,6 +8,9 @@
 #include "../../include/kfac_orthogonal.h"
 #include "../../include/kfac_tokens.h"
 
+#include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/variable.h>
+
 namespace {
 
 struct SamplePlan {
@@ -99,6 +102,17 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
     done(entries.lookup(&e, plan->base.ws, plan->base.ws_bytes, stream), "kfac_embedding_lookup");
     if (given) written(y);
     return THPVariable_Wrap(std::move(y));
+  });
+}
+
+// (tensor) -> whether a living graph adds up its gradient on the default stream.  A leaf's gradients are added where
+// the first of its living graphs was made, whatever operators they are of.
+PyObject* gathers_on_default(PyObject*, PyObject* t) {
+  return guarded([&]() -> PyObject* {
+    if (!THPVariable_Check(t)) throw Refused{KFAC_ERR_ARG, "not a tensor"};
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(THPVariable_Unpack(t));
+    const auto stream = node ? node->stream() : std::nullopt;
+    return PyBool_FromLong(stream && stream->id() == 0);
   });
 }
 
@@ -274,6 +288,7 @@ PyMethodDef methods[] = {{"bind", method(bind), METH_FASTCALL, nullptr},
                          {"plan_sizes", plan_sizes, METH_NOARGS, nullptr},
                          {"sample", method(sample), METH_FASTCALL, nullptr},
                          {"embedding", method(embedding), METH_FASTCALL, nullptr},
+                         {"gathers_on_default", gathers_on_default, METH_O, nullptr},
                          {"embedding_grad", method(embedding_grad), METH_FASTCALL, nullptr},
                          {"orthogonalize", method(orthogonalize), METH_FASTCALL, nullptr},
                          {"orthogonal_step", method(orthogonal_step), METH_FASTCALL, nullptr},

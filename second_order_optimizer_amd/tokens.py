@@ -19,7 +19,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import weakref
 from typing import Optional
 
 import torch
@@ -156,20 +155,13 @@ class Sampler(_Operator):
 class _EmbeddingNode(torch.autograd.Function):
     """The lookup's place in autograd: the table's gradient is dense."""
 
-    # Nodes made outside a capture on the default stream, while their graph lives.
-    _eager = weakref.WeakSet()
-
     @staticmethod
     def forward(ctx, table, ids, op, stream):
         # A leaf adds up its gradient on the stream where the first living graph found it, and the default
         # stream cannot take part in a capture: such a backward pass would end the process.
-        if torch.cuda.is_current_stream_capturing():
-            if any(node.table() is table for node in _EmbeddingNode._eager):
-                op._fail("a graph made on the default stream outside this capture still holds the table: drop its "
-                         "result first, or make it on another stream", KFAC_ERR_UNSUPPORTED)
-        elif table.is_leaf and torch.cuda.current_stream(table.device).cuda_stream == 0:
-            ctx.table = weakref.ref(table)
-            _EmbeddingNode._eager.add(ctx)
+        if torch.cuda.is_current_stream_capturing() and _native.gathers_on_default(table):
+            op._fail("a graph made on the default stream outside this capture still holds the table: drop its "
+                     "result first, or make it on another stream", KFAC_ERR_UNSUPPORTED)
         ctx.op = op
         ctx.save_for_backward(ids)
         return op.run(table, ids, None, stream)
@@ -213,8 +205,9 @@ class Embedding(_Operator):
         table [vocab, width] (any row stride), ids [rows] int32 or int64: a
         negative one gives a row of zeros, one of at least vocab too (flagged).
         out: where to write, for calls outside autograd.  Inside a capture
-        the call is refused while a graph of the same table lives that was
-        made on the default stream.
+        the call is refused while a graph of the same table lives, of this
+        operator or any other (tied weights), that was made on the default
+        stream.
         """
         if stream is None:
             y = _native.embedding(self._at, table, ids, out)

@@ -185,3 +185,29 @@ def test_capture_beside_a_graph_of_another_stream(gpu_lib):
         eager.backward(torch.ones_like(eager))
     torch.cuda.synchronize()
     assert torch.equal(table.grad, counts[:, None].expand(9, 16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("again", [False, True])
+def test_capture_refused_while_another_operator_holds_the_table(gpu_lib, again):
+    """Tied weights: the table is a projection's weight too, whose eager graph on the default stream still lives."""
+    op = T.Embedding(5, 9, 16, "f32")
+    table, ids = torch.randn(9, 16, device="cuda", requires_grad=True), torch.arange(5, device="cuda")
+    loss = torch.nn.functional.linear(torch.randn(4, 16, device="cuda"), table).sum()
+    if again:
+        loss = loss + op.run(table, ids).sum()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = torch.ones(3, device="cuda")                # (a graph of something)
+        with pytest.raises(K.KfacError) as e:
+            op.run(table, ids)
+    assert e.value.status == U and kept is not None
+    del loss
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = op.run(table, ids)
+        y.backward(torch.ones_like(y))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, table.detach()[:5]) and float(table.grad.sum()) == 5 * 16
