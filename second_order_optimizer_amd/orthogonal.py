@@ -138,12 +138,14 @@ class OrthogonalStep(_Iteration):
     """One step of a stack of layers (kfac_step_orthogonal gives the formulas).
 
     weights, momenta: float32 [d_out, d_in] each, contiguous, written in
-    place, in the memory that each tensor has when run() is called.  biases, bias_momenta: [d_out] each, or None for a layer without
-    one.  nesterov: whether the update looks ahead by the momentum.  scale:
-    the factor of a layer's step, "aspect" sqrt(max(1, d_out / d_in)), "rms"
-    0.2 sqrt(max(d_out, d_in)) or "none" 1.  products: "full" (the update as
-    exact as float32 products make it) or "half" (11 bits between the products,
-    a third of the operations; Orthogonal says how far off).
+    place, where each tensor's memory is when run() is called (a captured step
+    goes on writing where it was).  biases, bias_momenta: [d_out] each, or None
+    for a layer without one.  nesterov: whether the update looks ahead by the
+    momentum.  scale: the factor of a layer's step, "aspect" sqrt(max(1,
+    d_out / d_in)), "rms" 0.2 sqrt(max(d_out, d_in)) or "none" 1.  products:
+    "full" (the update as exact as float32 products make it) or "half" (11 bits
+    between the products, a third of the operations; Orthogonal says how far
+    off).
     """
 
     def __init__(self, weights: Sequence, momenta: Sequence, biases: Optional[Sequence] = None,
