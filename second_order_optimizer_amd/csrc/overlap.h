@@ -60,18 +60,20 @@ inline Lines lines_of(const void* p, int64_t run, int64_t rows = 1, int64_t ld =
   return {reinterpret_cast<uintptr_t>(p), run, rows, ld, mats, stride};
 }
 
-// Whether the two may share memory.  Not where their extents do not meet, nor where all
+// Whether the two share memory.  Not where their extents do not meet, nor where all
 // distances between their rows (or matrices) are multiples of one number, as between
 // column slices of a matrix (row slices of a batch), and the rows (matrices) lie apart
-// within it; what none of this shows apart counts as shared.
+// within it.  What that leaves is looked at row by row, if there are not too many (then
+// it counts as shared).
 inline bool overlap(const Lines& a, const Lines& b) {
   if (a.run < 1 || a.rows < 1 || a.mats < 1 || b.run < 1 || b.rows < 1 || b.mats < 1) return false;
   auto matrix = [](const Lines& l) { return l.run + (l.rows - 1) * l.ld; };
   auto extent = [&](const Lines& l) { return matrix(l) + (l.mats - 1) * l.stride; };
   if (a.begin + static_cast<uintptr_t>(extent(a)) <= b.begin || b.begin + static_cast<uintptr_t>(extent(b)) <= a.begin) return false;
+  const int64_t between = static_cast<int64_t>(b.begin - a.begin);
   auto apart = [&](int64_t a_run, int64_t b_run, int64_t step) {      // runs `step`, or a multiple of it, apart
     if (step == 0) return false;
-    const int64_t d = (static_cast<int64_t>(b.begin - a.begin) % step + step) % step;
+    const int64_t d = (between % step + step) % step;
     return d >= a_run && d + b_run <= step;
   };
   int64_t rows = 0, mats = 0;
@@ -79,7 +81,21 @@ inline bool overlap(const Lines& a, const Lines& b) {
     if (l->rows > 1) rows = std::gcd(rows, l->ld);
     if (l->mats > 1) mats = std::gcd(mats, l->stride);
   }
-  return !apart(a.run, b.run, std::gcd(rows, mats)) && !apart(matrix(a), matrix(b), mats);
+  if (apart(a.run, b.run, std::gcd(rows, mats)) || apart(matrix(a), matrix(b), mats)) return false;
+  constexpr int64_t most = 1 << 18;         // some 2 ms
+  if (a.mats > most / b.mats || a.rows > most / (a.mats * b.mats)) return true;
+  for (int64_t m = 0; m < a.mats; ++m)
+    for (int64_t n = 0; n < b.mats; ++n) {
+      const int64_t from = between + n * b.stride - m * a.stride;      // b's matrix, from a's
+      for (int64_t r = 0; r < a.rows; ++r) {
+        // the last of b's rows that begins before a's row ends: if none meets it, that one does not
+        const int64_t end = r * a.ld + a.run - 1 - from;
+        if (end < 0) continue;
+        const int64_t last = b.rows > 1 ? std::min(b.rows - 1, end / b.ld) : 0;
+        if (from + last * b.ld + b.run > r * a.ld) return true;
+      }
+    }
+  return false;
 }
 
 }  // namespace kfac

@@ -100,8 +100,7 @@ def test_update_beside_and_on_its_input(lib):
 
 
 def test_overlap_against_every_byte(tmp_path):
-    """csrc/overlap.h on small matrices: never apart where a byte is shared; never shared for column slices of one
-    matrix, or for what lies side by side, where none is."""
+    """csrc/overlap.h on small matrices says what their bytes say."""
     import itertools
     import shutil
     import subprocess
@@ -140,18 +139,14 @@ int main() {
             run, rows, mats = (int(rng.integers(0, n)) for n in (7, 5, 3))
             ld = run + int(rng.integers(0, 9))
             pair.append((1000 + int(rng.integers(0, 60)), run, rows, ld, mats, rows * ld + int(rng.integers(0, 9))))
-        cases.append((pair, False))
+        cases.append(pair)
     for a, b, at in itertools.product(range(1, 5), range(1, 5), range(0, 80, 3)):      # of one matrix of 11 columns
-        cases.append(([(1000, a, 4, 11, 1, 0), (1000 + at, b, 3, 11, 1, 0)], True))
-    text = "\n".join(" ".join(map(str, v)) for pair, _ in cases for v in pair)
+        cases.append([(1000, a, 4, 11, 1, 0), (1000 + at, b, 3, 11, 1, 0)])
+    text = "\n".join(" ".join(map(str, v)) for pair in cases for v in pair)
     out = subprocess.run([str(exe)], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
-    for (pair, exact), line in zip(cases, out):
-        shared, said = (v == "1" for v in line.split())
-        assert said or not shared, pair
-        (pa, ra, na, la, ma, _), (pb, rb, nb, lb, mb, _) = pair
-        inside = (pb - pa) % 11 + rb <= 11                              # the second matrix's rows are whole columns of the first's
-        if exact and inside and pb - pa < 33:
-            assert said == shared, pair
+    for pair, line in zip(cases, out):
+        shared, said = line.split()
+        assert said == shared, pair
     assert any(line == "0 0" for line in out) and any(line == "1 1" for line in out)
 
 
