@@ -200,3 +200,37 @@ def test_step_in_tiles_of_256(gpu_lib, products):
         # the weight's part: decay, product and sum are rounded, against an update of at most the weight's size
         close((0.875 * old[i].double() - w[i].double()) / 0.25, g[i], products, 16 * U)
     assert op.flags() == 0
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(130, 300, "bf16"), (130, 300, "f32"), (2047, 1000, "f32"), (1024, 8192, "f32"), (50, 900, "f32"),
+                                             (4000, 4090, "bf16"), (16384, 4096, "bf16"), (4096, 6000, "f32")])
+def test_update_after_others(gpu_lib, rows, cols, dtype):
+    """What a workspace holds of earlier calls, of numbers and of none, is in no later result."""
+    from second_order_optimizer_amd import orthogonal as M
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x, other = (torch.randn(rows, cols, generator=gen, device="cuda").to(DT[dtype]) for _ in range(2))
+    op = M.Orthogonal(rows, cols, dtype=dtype)
+    want = M.Orthogonal(rows, cols, dtype=dtype).run(x)
+    for before in (other, torch.full_like(other, np.nan), torch.full_like(other, 3e38)):
+        op.run(before)
+        assert torch.equal(op.run(x), want)
+
+
+def test_rows_after_others(gpu_lib):
+    """The same of the embedding's gradient and of sampling in parts."""
+    from second_order_optimizer_amd import tokens
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    for n in (5000, 70000):
+        emb, fresh = (tokens.Embedding(n, 3001, 130, "f32") for _ in range(2))
+        sets = [(torch.randn(n, 130, generator=gen, device="cuda"), (torch.rand(n, generator=gen, device="cuda") ** 2 * 3001).long()) for _ in range(2)]
+        want = fresh.backward(*sets[0])
+        for before in (sets[1], (torch.full_like(sets[1][0], np.nan), torch.full_like(sets[1][1], 7)), (sets[1][0], torch.full_like(sets[1][1], -1))):
+            emb.backward(*before)
+            assert all(torch.equal(a, b) for a, b in zip(emb.backward(*sets[0]), want))
+    sampler, fresh = (tokens.Sampler(3, 70000, top_k=50, top_p=0.9) for _ in range(2))
+    x, other = (torch.randn(3, 70000, generator=gen, device="cuda").bfloat16() * 3 for _ in range(2))
+    u = torch.rand(3, generator=gen, device="cuda")
+    want = fresh.run(x, u)
+    for before in (other, torch.full_like(other, np.nan), torch.full_like(other, -np.inf), torch.zeros_like(other)):
+        sampler.run(before, u)
+        assert all(torch.equal(a, b) for a, b in zip(sampler.run(x, u), want))
